@@ -396,6 +396,96 @@ int usp_dilated_attn_fwd(const void* q, const void* k, const void* v, void* out,
                          size_t ws_bytes, void* stream);
 
 /*
+ * Causal attention with a sliding window and sinks (the pattern of a long-context
+ * model's local layers; the pages name sparse attention without a pattern), over
+ * the global layout: query i of a sequence of S tokens sees key j iff
+ *     lo_i <= j <= i   and   (i - j < window  or  j - lo_i < sinks),
+ * i.e. its own and the window - 1 keys before it, and the first `sinks` keys of
+ * its document (lo_i: the document's first token; without cu_seqlens, 0).
+ *   q            [B][S][Hq][D]  bf16;  k, v [B][S][Hkv][D] bf16 (query head h
+ *                attends kv head h / (Hq/Hkv))
+ *   out          [B][S][Hq][D]  bf16;  lse [B][S][Hq] fp32, natural log
+ *   window       >= 1 (S or more: plain causal attention)
+ *   sinks        0 .. USP_WINDOW_MAX_SINKS
+ *   cu_seqlens   DEVICE int32 [n_docs + 1] as for usp_attn_fwd_masked (packed
+ *                documents shared by the batch, cu[0] = 0, cu[n_docs] = S), or
+ *                NULL (then n_docs is ignored). Other values give undefined
+ *                results but never an access outside the tensors.
+ *   workspace    usp_window_workspace_size(..., n_docs, bwd) bytes (n_docs = 0
+ *                without documents): the status header; for the backward also the
+ *                row tables and the sums of the sinks' gradients
+ * Any S >= 1; D in {64, 128}; scale 1/sqrt(D). Elements must be finite, those of
+ * hidden keys too (a hidden key has weight 0, and 0 times infinity is NaN).
+ *
+ * usp_window_attn_bwd: the gradients, from the forward's out and lse: dQ, dK, dV
+ * in bf16, each element its fp32 sum rounded once (dK, dV summed over the heads of
+ * a group). Overwritten, deterministic.
+ */
+#define USP_WINDOW_MAX_SINKS 128
+size_t usp_window_workspace_size(int B, int S, int Hq, int Hkv, int D, int window, int sinks, int n_docs, int bwd);
+int usp_window_attn_fwd(const void* q, const void* k, const void* v, void* out, float* lse, int B, int S, int Hq,
+                        int Hkv, int D, int window, int sinks, const int* cu_seqlens, int n_docs, void* workspace,
+                        size_t ws_bytes, void* stream);
+int usp_window_attn_bwd(const void* q, const void* k, const void* v, const void* out, const float* lse,
+                        const void* dO, void* dQ, void* dK, void* dV, int B, int S, int Hq, int Hkv, int D, int window,
+                        int sinks, const int* cu_seqlens, int n_docs, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * The same attention for the newest n tokens of each of N sequences over a cache
+ * that already holds them: token t of sequence s sits at position
+ * lens[s] - n + t and sees the cached keys of the rule above.
+ *   q            [N][n][Hq][D] bf16, 1 <= n <= USP_WINDOW_MAX_NEW
+ *   k_cache, v_cache  bf16, row of key j, kv head h of sequence s at
+ *                s * k_sn + j * k_st + h * k_sh elements (v alike): [N][cap][Hkv][D],
+ *                [N][Hkv][cap][D] or a slice of such; strides multiples of 8
+ *                elements, rows of D contiguous elements
+ *   lens         DEVICE int32 [N], cached tokens 0 .. cap (values outside are
+ *                taken as the nearer end); rows past lens are never read
+ *   out          [N][n][Hq][D] bf16;  lse [N][n][Hq] fp32. A token at a negative
+ *                position (lens[s] < n) sees nothing: out = 0, lse = -inf.
+ *   workspace    usp_window_decode_workspace_size(...) bytes (fp32 partials of the
+ *                splits; no status is kept: the kernels wait for nothing)
+ */
+#define USP_WINDOW_MAX_NEW 16
+size_t usp_window_decode_workspace_size(int N, int n, int cap, int Hq, int Hkv, int D, int window, int sinks);
+int usp_window_attn_decode(const void* q, const void* k_cache, const void* v_cache, const int* lens, void* out,
+                           float* lse, int N, int n, int cap, int Hq, int Hkv, int D, int window, int sinks,
+                           long long k_sn, long long k_st, long long k_sh, long long v_sn, long long v_st,
+                           long long v_sh, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Rotary positions with several axes (time, height, width of a token): the first
+ * R elements of every head row are R/2 pairs, and pair f turns by
+ *     a = positions[axis[f]][b][t] * inv_freq[f]:
+ *     y1 = x1 cos a - x2 sin a,   y2 = x2 cos a + x1 sin a;
+ * elements R .. D-1 are copied. inverse = 1 turns by -a: the gradient's map.
+ *   jobs         HOST array of 1 .. USP_MAX_ROPE_JOBS tensors of one element type
+ *                (e.g. q and k): row of head h, token t, sequence b at
+ *                b * s_b + t * s_t + h * s_h elements of src (so a slice of a fused
+ *                projection, or a broadcast by stride 0), likewise d_* of dst; rows
+ *                of D contiguous elements. dst may be src with the same strides;
+ *                any other overlap is undefined.
+ *   dtype        USP_BF16 or USP_F32 (arithmetic in fp32, rounded once)
+ *   positions    DEVICE integers [n_axes][B][S], 32 or 64 bits (pos_bits); any sign
+ *   inv_freq     HOST [R/2], radians per position step, finite
+ *   axis         HOST [R/2], 0 .. n_axes-1
+ *   paired       0: pairs (f, f + R/2); 1: pairs (2f, 2f + 1)
+ * The layout does not matter: on rank-major or zigzag tensors, give the positions
+ * in the same order. inv_freq and axis are read before the call returns.
+ */
+#define USP_MAX_ROPE_JOBS 4
+#define USP_ROPE_MAX_R 256
+typedef struct {
+  const void* src;
+  void* dst;
+  int H;
+  long long s_b, s_t, s_h, d_b, d_t, d_h;
+} usp_rope_job;
+int usp_rope_axes(const usp_rope_job* jobs, int n_jobs, int B, int S, int D, int R, int dtype, const void* positions,
+                  int pos_bits, int n_axes, const double* inv_freq, const int* axis, int paired, int inverse,
+                  void* stream);
+
+/*
  * usp_rows_copy: up to USP_MAX_ROWS_JOBS affine row copies in one launch, the
  * data movement around the LongNet collectives below (packing the kept rows of
  * a rank before an all-gather, compacting the gathered blocks, and the reverse

@@ -269,3 +269,192 @@ def bwd_preprocess(out: torch.Tensor, dO: torch.Tensor, stream=None) -> torch.Te
     delta = torch.empty(out.shape[:-1], dtype=torch.float32, device=out.device)
     B_.usp_bwd_preprocess(out, dO, delta, rows, D, stream)
     return delta
+
+
+def _check(name: str, t: torch.Tensor, ref: torch.Tensor, dtype, shape=None, contiguous=True) -> torch.Tensor:
+    """An argument of the calls below: a tensor of ref's device with this type and shape."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != ref.device:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the first one")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, not {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+class _on:
+    """The device of `ref` and the stream that a call runs on: ref's device's current stream, or
+    the given one. What the call allocates inside belongs to that stream, and the inputs are kept
+    from the allocator until its work on them is done."""
+
+    def __init__(self, ref: torch.Tensor, stream, *inputs):
+        self.ctx = None
+        if stream is not None:
+            s = torch.cuda.ExternalStream(stream, ref.device) if isinstance(stream, int) else stream
+            if s.device != ref.device:
+                raise ValueError("the stream is of another device than the tensors")
+            for t in inputs:
+                if t is not None:
+                    t.record_stream(s)
+            self.ctx = torch.cuda.stream(s)
+        elif ref.device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(ref.device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *a):
+        if self.ctx is not None:
+            self.ctx.__exit__(*a)
+
+
+def _scratch(ws, nbytes: int, ref: torch.Tensor) -> torch.Tensor:
+    """The given workspace, or a new one (the calls below clear what they need of it)."""
+    if ws is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=ref.device)
+    return _check("ws", ws, ref, torch.uint8)
+
+
+def _new(t, name: str, shape, dtype, ref: torch.Tensor) -> torch.Tensor:
+    return torch.empty(shape, dtype=dtype, device=ref.device) if t is None else _check(name, t, ref, dtype, shape)
+
+
+def _window_geometry(q, k, v, window, sinks, cu_seqlens):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B, S, Hq, D] and k, v [B, S, Hkv, D]")
+    B, S, Hq, D = q.shape
+    Hkv = k.shape[2]
+    _check("q", q, q, torch.bfloat16)
+    _check("k", k, q, torch.bfloat16, (B, S, Hkv, D))
+    _check("v", v, q, torch.bfloat16, (B, S, Hkv, D))
+    n_docs = 0
+    if cu_seqlens is not None:
+        _check("cu_seqlens", cu_seqlens, q, torch.int32)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be [n_docs + 1]")
+        n_docs = cu_seqlens.numel() - 1
+    return (B, S, Hq, Hkv, D, int(window), int(sinks)), n_docs
+
+
+def _ws_bytes(n: int, what: str, *geometry) -> int:
+    if n == 0:
+        raise B_.UspError(B_.USP_ERR_UNSUPPORTED, f"{what}{geometry}: {B_.usp_last_error()}")
+    return n
+
+
+def window_attn_fwd(q, k, v, window: int, sinks: int = 0, cu_seqlens=None, ws=None, out=None, lse=None, stream=None,
+                    check_status: bool = False):
+    """Causal attention with a sliding window and sinks over global-layout q [B, S, Hq, D], k/v
+    [B, S, Hkv, D] (bf16): query i sees its own and the window - 1 keys before it, and the first
+    `sinks` keys; with cu_seqlens ([n_docs + 1] int32, CUDA) all within its document. Returns
+    (out bf16 like q, lse fp32 [B, S, Hq]). Elements must be finite, hidden ones too."""
+    geo, n_docs = _window_geometry(q, k, v, window, sinks, cu_seqlens)
+    need = _ws_bytes(B_.usp_window_workspace_size(*geo, n_docs, 0), "window attention", *geo)
+    with _on(q, stream, q, k, v, cu_seqlens, ws, out, lse) as st:
+        out = _new(out, "out", q.shape, torch.bfloat16, q)
+        lse = _new(lse, "lse", q.shape[:-1], torch.float32, q)
+        ws = _scratch(ws, need, q)
+        B_.usp_window_attn_fwd(q, k, v, out, lse, *geo, cu_seqlens, n_docs, ws, ws.numel(), st)
+        if check_status:
+            check_workspace(ws, st)
+    return out, lse
+
+
+def window_attn_bwd(q, k, v, out, lse, dO, window: int, sinks: int = 0, cu_seqlens=None, ws=None, dq=None, dk=None,
+                    dv=None, stream=None, check_status: bool = False):
+    """Backward of window_attn_fwd from its out and lse; returns (dQ, dK, dV) in bf16, like q, k, v."""
+    geo, n_docs = _window_geometry(q, k, v, window, sinks, cu_seqlens)
+    _check("out", out, q, torch.bfloat16, q.shape)
+    _check("dO", dO, q, torch.bfloat16, q.shape)
+    _check("lse", lse, q, torch.float32, q.shape[:-1])
+    need = _ws_bytes(B_.usp_window_workspace_size(*geo, n_docs, 1), "window attention", *geo)
+    with _on(q, stream, q, k, v, out, lse, dO, cu_seqlens, ws, dq, dk, dv) as st:
+        dq = _new(dq, "dq", q.shape, torch.bfloat16, q)
+        dk = _new(dk, "dk", k.shape, torch.bfloat16, q)
+        dv = _new(dv, "dv", v.shape, torch.bfloat16, q)
+        ws = _scratch(ws, need, q)
+        B_.usp_window_attn_bwd(q, k, v, out, lse, dO, dq, dk, dv, *geo, cu_seqlens, n_docs, ws, ws.numel(), st)
+        if check_status:
+            check_workspace(ws, st)
+    return dq, dk, dv
+
+
+def window_attn_decode(q, k_cache, v_cache, lens, window: int, sinks: int = 0, ws=None, out=None, lse=None,
+                       stream=None):
+    """The attention of window_attn_fwd for the newest n tokens q [N, n, Hq, D] of N sequences whose
+    caches k_cache, v_cache [N, cap, Hkv, D] (any strides, the last dimension contiguous) already hold
+    them, lens [N] int32 (CUDA) tokens each. Returns (out bf16 like q, lse fp32 [N, n, Hq]); a token at
+    a negative position (lens < n: an idle slot) gets out = 0, lse = -inf. Cache rows past lens are
+    never read."""
+    if q.dim() != 4 or k_cache.dim() != 4:
+        raise ValueError("q must be [N, n, Hq, D] and the caches [N, cap, Hkv, D]")
+    N, n, Hq, D = q.shape
+    cap, Hkv = k_cache.shape[1], k_cache.shape[2]
+    _check("q", q, q, torch.bfloat16)
+    _check("k_cache", k_cache, q, torch.bfloat16, (N, cap, Hkv, D), contiguous=False)
+    _check("v_cache", v_cache, q, torch.bfloat16, (N, cap, Hkv, D), contiguous=False)
+    _check("lens", lens, q, torch.int32, (N,))
+    ks, vs = k_cache.stride(), v_cache.stride()
+    if ks[3] != 1 or vs[3] != 1:
+        raise ValueError("the last dimension of the caches must be contiguous")
+    geo = (N, n, cap, Hq, Hkv, D, int(window), int(sinks))
+    need = _ws_bytes(B_.usp_window_decode_workspace_size(*geo), "window decode", *geo)
+    with _on(q, stream, q, k_cache, v_cache, lens, ws, out, lse) as st:
+        out = _new(out, "out", q.shape, torch.bfloat16, q)
+        lse = _new(lse, "lse", q.shape[:-1], torch.float32, q)
+        ws = _scratch(ws, need, q)
+        B_.usp_window_attn_decode(q, k_cache, v_cache, lens, out, lse, *geo, ks[:3], vs[:3], ws, ws.numel(), st)
+    return out, lse
+
+
+def rope_axes(xs, positions, inv_freq, axis, paired: bool = False, inverse: bool = False, outs=None, stream=None):
+    """Rotary positions with several axes of the tensors xs (one or a sequence, [B, S, H_x, D], bf16 or
+    fp32, any strides with the last dimension contiguous, e.g. q and k sliced from a fused projection),
+    in one launch: pair f of every head row turns by positions[axis[f]] * inv_freq[f]. positions
+    [n_axes, B, S] int32 or int64 (CUDA); inv_freq [R/2] float64 and axis [R/2] int32 on the CPU (R <= D;
+    elements from R on are copied). paired: pairs (2f, 2f + 1) instead of (f, f + R/2). inverse: the
+    gradient's map. outs: where to write (may be xs: in place); else new contiguous tensors. Returns the
+    list of outputs (one tensor for one tensor)."""
+    single = isinstance(xs, torch.Tensor)
+    xs = (xs,) if single else tuple(xs)
+    if not xs or len(xs) > B_.USP_MAX_ROPE_JOBS:
+        raise ValueError(f"one to {B_.USP_MAX_ROPE_JOBS} tensors")
+    x0 = xs[0]
+    dt = _dt(x0)
+    if x0.dim() != 4:
+        raise ValueError("tensors must be [B, S, H, D]")
+    B, S, _, D = x0.shape
+    for x in xs:
+        if x.dim() != 4:
+            raise ValueError("tensors must be [B, S, H, D]")
+        _check("x", x, x0, x0.dtype, (B, S, x.shape[2], D), contiguous=False)
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise TypeError("positions must be int32 or int64")
+    _check("positions", positions, x0, positions.dtype)
+    if positions.dim() != 3 or positions.shape[1:] != (B, S):
+        raise ValueError(f"positions must be [n_axes, {B}, {S}]")
+    for name, t, want in (("inv_freq", inv_freq, torch.float64), ("axis", axis, torch.int32)):
+        if t.device.type != "cpu" or t.dtype != want or t.dim() != 1 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous 1-D {want} tensor on the CPU")
+    if inv_freq.numel() != axis.numel():
+        raise ValueError("inv_freq and axis must have one entry per frequency")
+    outs = ((outs,) if single else tuple(outs)) if outs is not None else (None,) * len(xs)
+    if len(outs) != len(xs):
+        raise ValueError("one output per tensor")
+    with _on(x0, stream, positions, *xs, *outs) as st:
+        ys, jobs = [], []
+        for x, y in zip(xs, outs):
+            y = (torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None
+                 else _check("out", y, x0, x.dtype, x.shape, contiguous=False))
+            sx, sy = x.stride(), y.stride()
+            if D > 1 and (sx[3] != 1 or sy[3] != 1):
+                raise ValueError("the last dimension must be contiguous")
+            ys.append(y)
+            jobs.append((x, y, x.shape[2], sx[:3], sy[:3]))
+        B_.usp_rope_axes(jobs, B, S, D, 2 * inv_freq.numel(), dt, positions, 8 * positions.element_size(),
+                         positions.shape[0], inv_freq, axis, paired, inverse, st)
+    return ys[0] if single else ys

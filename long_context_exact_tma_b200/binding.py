@@ -35,6 +35,10 @@ USP_MAP_PACK_TOKENS = 6
 USP_MAP_UNPACK_HEADS = 7
 USP_DILATED_MAX_PAIRS = 16
 USP_MAX_ROWS_JOBS = 16
+USP_MAX_ROPE_JOBS = 4
+USP_ROPE_MAX_R = 256
+USP_WINDOW_MAX_SINKS = 128
+USP_WINDOW_MAX_NEW = 16
 
 
 class AttnMask(ctypes.Structure):
@@ -52,6 +56,13 @@ class RowsJob(ctypes.Structure):
                 ("d_b", ctypes.c_longlong), ("d_k", ctypes.c_longlong), ("d_h", ctypes.c_longlong),
                 ("d_k0", ctypes.c_int), ("d_kstep", ctypes.c_int), ("d_h0", ctypes.c_int), ("d_hstep", ctypes.c_int),
                 ("d_hdiv", ctypes.c_int)]
+
+
+class RopeJob(ctypes.Structure):
+    """usp_rope_job of include/usp.h."""
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("H", ctypes.c_int),
+                ("s_b", ctypes.c_longlong), ("s_t", ctypes.c_longlong), ("s_h", ctypes.c_longlong),
+                ("d_b", ctypes.c_longlong), ("d_t", ctypes.c_longlong), ("d_h", ctypes.c_longlong)]
 
 
 class PermuteJob(ctypes.Structure):
@@ -86,6 +97,12 @@ SIGNATURES = {
     "usp_dilated_attn_fwd": (_I, [_P] * 5 + [_I] * 7 + [_P, _P, _P, _SZ, _P]),
     "usp_dilated_bwd_workspace_size": (_SZ, [_I] * 5 + [_P, _P]),
     "usp_dilated_attn_bwd": (_I, [_P] * 9 + [_I] * 7 + [_P, _P, _P, _SZ, _P]),
+    "usp_window_workspace_size": (_SZ, [_I] * 9),
+    "usp_window_attn_fwd": (_I, [_P] * 5 + [_I] * 7 + [_P, _I, _P, _SZ, _P]),
+    "usp_window_attn_bwd": (_I, [_P] * 9 + [_I] * 7 + [_P, _I, _P, _SZ, _P]),
+    "usp_window_decode_workspace_size": (_SZ, [_I] * 8),
+    "usp_window_attn_decode": (_I, [_P] * 6 + [_I] * 8 + [_LL] * 6 + [_P, _SZ, _P]),
+    "usp_rope_axes": (_I, [ctypes.POINTER(RopeJob)] + [_I] * 6 + [_P, _I, _I, _P, _P, _I, _I, _P]),
     "usp_rows_copy": (_I, [ctypes.POINTER(RowsJob), _I, _P]),
     "usp_longnet_rows": (_I, [_I] * 5 + [_P] * 4),
     "usp_longnet_workspace_size": (_SZ, [_I] * 5 + [_P, _P, _I]),
@@ -280,6 +297,50 @@ def usp_dilated_attn_bwd(q, k, v, out, lse, dO, dQ, dK, dV, B, S, Hq, Hkv, D, ca
     rc = lib().usp_dilated_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dO), _ptr(dQ), _ptr(dK),
                                     _ptr(dV), B, S, Hq, Hkv, D, int(causal), n, w, r, _ptr(workspace), ws_bytes,
                                     _stream(stream))
+    return _check(rc) if check else rc
+
+
+def usp_window_workspace_size(B, S, Hq, Hkv, D, window, sinks, n_docs, bwd) -> int:
+    return int(lib().usp_window_workspace_size(B, S, Hq, Hkv, D, window, sinks, n_docs, int(bwd)))
+
+
+def usp_window_attn_fwd(q, k, v, out, lse, B, S, Hq, Hkv, D, window, sinks, cu_seqlens, n_docs, workspace, ws_bytes,
+                        stream=None, check=True):
+    rc = lib().usp_window_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, S, Hq, Hkv, D, window, sinks,
+                                   _ptr(cu_seqlens), n_docs, _ptr(workspace), ws_bytes, _stream(stream))
+    return _check(rc) if check else rc
+
+
+def usp_window_attn_bwd(q, k, v, out, lse, dO, dQ, dK, dV, B, S, Hq, Hkv, D, window, sinks, cu_seqlens, n_docs,
+                        workspace, ws_bytes, stream=None, check=True):
+    rc = lib().usp_window_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dO), _ptr(dQ), _ptr(dK),
+                                   _ptr(dV), B, S, Hq, Hkv, D, window, sinks, _ptr(cu_seqlens), n_docs,
+                                   _ptr(workspace), ws_bytes, _stream(stream))
+    return _check(rc) if check else rc
+
+
+def usp_window_decode_workspace_size(N, n, cap, Hq, Hkv, D, window, sinks) -> int:
+    return int(lib().usp_window_decode_workspace_size(N, n, cap, Hq, Hkv, D, window, sinks))
+
+
+def usp_window_attn_decode(q, k_cache, v_cache, lens, out, lse, N, n, cap, Hq, Hkv, D, window, sinks, k_strides,
+                           v_strides, workspace, ws_bytes, stream=None, check=True):
+    """k_strides, v_strides: (sequence, token, head) strides of the caches in elements."""
+    rc = lib().usp_window_attn_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(lens), _ptr(out), _ptr(lse), N, n,
+                                      cap, Hq, Hkv, D, window, sinks, *k_strides, *v_strides, _ptr(workspace),
+                                      ws_bytes, _stream(stream))
+    return _check(rc) if check else rc
+
+
+def usp_rope_axes(jobs, B, S, D, R, dtype, positions, pos_bits, n_axes, inv_freq, axis, paired, inverse, stream=None,
+                  check=True):
+    """jobs: sequence of (src, dst, H, (s_b, s_t, s_h), (d_b, d_t, d_h)); inv_freq (float64) and axis (int32) in
+    host memory: CPU tensors or addresses."""
+    arr = (RopeJob * max(len(jobs), 1))()
+    for x, (src, dst, H, ss, ds) in enumerate(jobs):
+        arr[x] = RopeJob(_ptr(src), _ptr(dst), H, *ss, *ds)
+    rc = lib().usp_rope_axes(arr, len(jobs), B, S, D, R, dtype, _ptr(positions), pos_bits, n_axes, _ptr(inv_freq),
+                             _ptr(axis), int(paired), int(inverse), _stream(stream))
     return _check(rc) if check else rc
 
 

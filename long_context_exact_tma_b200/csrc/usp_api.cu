@@ -169,6 +169,12 @@ int make_tmap_strided_h(CUtensorMap* m, const void* base, int D, int H, long lon
 }
 unsigned long long current_wait_ns() { return g_wait_ns; }
 
+int sm_count() {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
 namespace {
 struct SidePool {
   int dev = -1;

@@ -210,4 +210,39 @@ int dilated_bwd_pair(const void* q, const void* k, const void* v, const void* dO
                      int S, int Hq, int Hkv, int D, int causal, int w, int r, int* status, cudaStream_t st,
                      int first = 0);
 
+// Sliding-window attention with sinks (usp_window*.cu): the problem's geometry.
+struct WinGeo {
+  int B, S, Hq, Hkv, G;
+  int W, ns;      // window (1 .. S) and sinks (0 .. S)
+  const int* cu;  // [n_docs + 1] document boundaries, or null
+  int n_docs;
+  int n_tiles;    // 128-row tiles of the sequence
+  int pair_heads; // forward: a CTA's two query tiles are two heads of a group (else two row tiles of a head)
+  float scale, scale_log2;
+};
+
+struct WinLaunch {
+  WinGeo g;
+  int D;
+  CUtensorMap tm_q, tm_k, tm_v, tm_do;
+  void* out;
+  float* lse;
+  void *dq, *dk, *dv;          // bf16
+  const float *lse2, *delta;   // [B*Hq][Lp]: -LSE*log2(e), -Delta (launch_bwd_prep_rows)
+  int Lp;
+  const void *q, *k, *v, *dO;  // the tensors behind the maps (far sinks)
+  float* far_part;             // [B][Hkv][n_tiles][ns][2][D]
+  float* far_sum;              // [B][Hkv][n_docs][ns][2][D], null without sinks
+  int* status;
+  unsigned long long wait_ns;
+};
+cudaError_t launch_window_fwd(const WinLaunch& L, cudaStream_t stream);
+cudaError_t launch_window_dkdv(const WinLaunch& L, cudaStream_t stream);
+cudaError_t launch_window_dq(const WinLaunch& L, cudaStream_t stream);
+// dK, dV of the sinks from the queries outside their key tile's band: far_part, then far_sum.
+cudaError_t launch_window_far(const WinLaunch& L, cudaStream_t stream);
+
+// The current device's multiprocessor count.
+int sm_count();
+
 }  // namespace usp

@@ -1,0 +1,254 @@
+// usp_rope.cu -- rotary positions with several axes (time, height, width): every
+// frequency f of a head row takes its position from one of the axes,
+//   a = position[axis(f)] * inv_freq[f],
+//   y1 = x1 cos a - x2 sin a,  y2 = x2 cos a + x1 sin a
+// for the pair (x1, x2) = elements (f, f + R/2) or (2f, 2f + 1); elements from R
+// on are copied. The inverse (the gradient's map) turns by -a.
+//
+// The angle of a far position needs more bits than fp32 has (at position 10^5 an
+// fp32 product is off by 4e-3 rad). Here it is counted in turns on 64 bits: the
+// host gives inv_freq / 2 pi as a 64-bit fraction of a turn, and the wrapping
+// 64-bit product with the position keeps the fraction of the turn exactly; its
+// upper 32 bits, as a signed number, are the angle within half a turn.
+//
+// Bound by memory: each element is read and written once. A thread takes one
+// 16-byte chunk column (two in the halves form) of one token and walks some of its
+// heads, so that the sines are computed once per walk; the lanes of a warp cover
+// neighbouring chunks and heads. Views whose rows are not 16-byte aligned take the
+// same kernel with one-element chunks.
+#include <math.h>
+
+#include "../../include/usp.h"
+#include "usp_internal.h"
+#include "usp_ptx.cuh"
+
+namespace usp {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxFreq = USP_ROPE_MAX_R / 2;
+constexpr int kHeadsPerThread = 8;
+
+struct Job {
+  const void* src;
+  void* dst;
+  int H, groups, g0;  // heads; threads that share a token's heads; the first of them
+  long long s_b, s_t, s_h, d_b, d_t, d_h;
+};
+
+struct RopeArgs {
+  Job job[USP_MAX_ROPE_JOBS];
+  int n_jobs, S, D, R, groups, pos64, inverse;
+  long long units;      // (token, group, chunk)
+  long long axis_step;  // tokens per axis of the position table
+  const void* pos;
+  unsigned long long turn[kMaxFreq];  // inv_freq / 2 pi as a fraction of 2^64
+  unsigned char axis[kMaxFreq];
+};
+
+template <class T, int V>
+struct Chunk {
+  T e[V];
+};
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <class T>
+__device__ __forceinline__ T narrow(float x) {
+  if constexpr (sizeof(T) == 4)
+    return x;
+  else
+    return __float2bfloat16_rn(x);  // the one rounding of the output
+}
+template <class T, int V>
+__device__ __forceinline__ Chunk<T, V> load(const T* p) {
+  Chunk<T, V> c;
+  if constexpr (V * sizeof(T) == 16)
+    *reinterpret_cast<uint4*>(&c) = *reinterpret_cast<const uint4*>(p);
+  else
+    for (int x = 0; x < V; ++x) c.e[x] = p[x];
+  return c;
+}
+template <class T, int V>
+__device__ __forceinline__ void store(T* p, const Chunk<T, V>& c) {
+  if constexpr (V * sizeof(T) == 16)
+    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(&c);
+  else
+    for (int x = 0; x < V; ++x) p[x] = c.e[x];
+}
+
+// kPaired: a chunk of kV elements holds kV / 2 whole pairs; else it is kV first
+// elements, whose partners lie R / 2 on.
+template <class T, int kV, bool kPaired>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int kF = kPaired ? (kV + 1) / 2 : kV;  // frequencies of a chunk
+  constexpr int kW = kPaired ? 2 * kF : kV;        // elements of a chunk
+  __shared__ unsigned long long s_turn[kMaxFreq];
+  __shared__ unsigned char s_axis[kMaxFreq];
+  for (int x = threadIdx.x; x < a.R / 2; x += kThreads) {
+    s_turn[x] = a.turn[x];
+    s_axis[x] = a.axis[x];
+  }
+  __syncthreads();
+  const int n_rot = a.R / 2 / kF, n_chunks = n_rot + (a.D - a.R) / kV;
+  const long long u = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+  if (u >= a.units) return;
+  const int chunk = static_cast<int>(u % n_chunks);
+  const long long r = u / n_chunks;
+  const int grp = static_cast<int>(r % a.groups);
+  const long long token = r / a.groups;
+  const long long b = token / a.S, t = token % a.S;
+  int j = 0;
+  while (j + 1 < a.n_jobs && grp >= a.job[j + 1].g0) ++j;
+  const Job& job = a.job[j];
+  const int h0 = grp - job.g0;
+  const T* src = static_cast<const T*>(job.src) + b * job.s_b + t * job.s_t;
+  T* dst = static_cast<T*>(job.dst) + b * job.d_b + t * job.d_t;
+  if (chunk >= n_rot) {  // not rotated
+    const int e = a.R + (chunk - n_rot) * kV;
+    if (src == dst && job.s_h == job.d_h) return;
+    for (int h = h0; h < job.H; h += job.groups)
+      store<T, kV>(dst + h * job.d_h + e, load<T, kV>(src + h * job.s_h + e));
+    return;
+  }
+  float c[kF], s[kF];
+#pragma unroll
+  for (int f = 0; f < kF; ++f) {
+    const int fr = chunk * kF + f;
+    const long long at = s_axis[fr] * a.axis_step + token;
+    const long long p = a.pos64 ? static_cast<const long long*>(a.pos)[at] : static_cast<const int*>(a.pos)[at];
+    const unsigned long long turn = s_turn[fr] * static_cast<unsigned long long>(p);
+    const float half_turns = static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f;  // 2^-31
+    if constexpr (sizeof(T) == 4) {
+      sincospif(half_turns, &s[f], &c[f]);
+    } else {  // absolute error below 2^-20 in [-pi, pi], far below bf16's rounding
+      __sincosf(half_turns * 3.14159265358979f, &s[f], &c[f]);
+    }
+    if (a.inverse) s[f] = -s[f];
+  }
+  const int e1 = kPaired ? chunk * kW : chunk * kV, e2 = e1 + a.R / 2;
+#pragma unroll 4
+  for (int h = h0; h < job.H; h += job.groups) {
+    if constexpr (kPaired) {
+      Chunk<T, kW> x = load<T, kW>(src + h * job.s_h + e1);
+#pragma unroll
+      for (int f = 0; f < kF; ++f) {
+        const float x1 = widen(x.e[2 * f]), x2 = widen(x.e[2 * f + 1]);
+        x.e[2 * f] = narrow<T>(x1 * c[f] - x2 * s[f]);
+        x.e[2 * f + 1] = narrow<T>(x2 * c[f] + x1 * s[f]);
+      }
+      store<T, kW>(dst + h * job.d_h + e1, x);
+    } else {
+      Chunk<T, kV> y1 = load<T, kV>(src + h * job.s_h + e1), y2 = load<T, kV>(src + h * job.s_h + e2);
+#pragma unroll
+      for (int f = 0; f < kF; ++f) {
+        const float x1 = widen(y1.e[f]), x2 = widen(y2.e[f]);
+        y1.e[f] = narrow<T>(x1 * c[f] - x2 * s[f]);
+        y2.e[f] = narrow<T>(x2 * c[f] + x1 * s[f]);
+      }
+      store<T, kV>(dst + h * job.d_h + e1, y1);
+      store<T, kV>(dst + h * job.d_h + e2, y2);
+    }
+  }
+}
+
+template <class T, int kV, bool kPaired>
+cudaError_t launch(RopeArgs& a, long long tokens, cudaStream_t st) {
+  constexpr int kF = kPaired ? (kV + 1) / 2 : kV;
+  const long long n_chunks = a.R / 2 / kF + (a.D - a.R) / kV;
+  // Heads per thread: as many as pay the sines back, fewer while the tokens alone do not fill the machine.
+  int per = kHeadsPerThread;
+  auto groups_at = [&](int hp) {
+    int n = 0;
+    for (int j = 0; j < a.n_jobs; ++j) n += (a.job[j].H + hp - 1) / hp;
+    return n;
+  };
+  while (per > 1 && tokens * n_chunks * groups_at(per) < 148LL * 1024) per /= 2;
+  a.groups = 0;
+  for (int j = 0; j < a.n_jobs; ++j) {
+    a.job[j].g0 = a.groups;
+    a.job[j].groups = (a.job[j].H + per - 1) / per;
+    a.groups += a.job[j].groups;
+  }
+  a.units = tokens * n_chunks * a.groups;
+  const long long blocks = (a.units + kThreads - 1) / kThreads;
+  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+  rope_kernel<T, kV, kPaired><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(a);
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace usp
+
+using namespace usp;
+
+extern "C" int usp_rope_axes(const usp_rope_job* jobs, int n_jobs, int B, int S, int D, int R, int dtype,
+                             const void* positions, int pos_bits, int n_axes, const double* inv_freq, const int* axis,
+                             int paired, int inverse, void* stream) {
+  if (!jobs || !positions || !inv_freq || !axis) return record_error(USP_ERR_INVALID_ARG, "null pointer");
+  if (n_jobs < 1 || n_jobs > USP_MAX_ROPE_JOBS)
+    return record_error(USP_ERR_INVALID_ARG, "n_jobs must be 1..%d", USP_MAX_ROPE_JOBS);
+  if (B <= 0 || S <= 0 || D <= 0) return record_error(USP_ERR_INVALID_ARG, "sizes must be positive");
+  if (dtype != USP_BF16 && dtype != USP_F32) return record_error(USP_ERR_INVALID_ARG, "dtype must be USP_BF16 or USP_F32");
+  if (pos_bits != 32 && pos_bits != 64) return record_error(USP_ERR_INVALID_ARG, "pos_bits must be 32 or 64");
+  if (reinterpret_cast<uintptr_t>(positions) % (pos_bits / 8))
+    return record_error(USP_ERR_INVALID_ARG, "misaligned positions");
+  if ((paired | inverse) & ~1) return record_error(USP_ERR_INVALID_ARG, "paired and inverse must be 0 or 1");
+  if (n_axes < 1 || n_axes > 255) return record_error(USP_ERR_INVALID_ARG, "n_axes must be 1..255");
+  if (R < 2 || R % 2 || R > D || R > USP_ROPE_MAX_R)
+    return record_error(USP_ERR_UNSUPPORTED, "R must be even, 2..min(D, %d) (got %d)", USP_ROPE_MAX_R, R);
+  const int es = dtype == USP_BF16 ? 2 : 4;
+  RopeArgs a{};
+  // whole 16-byte chunks everywhere, or single elements
+  const int V = 16 / es;
+  bool wide = D % V == 0 && (paired ? R % V == 0 : (R / 2) % V == 0);
+  for (int x = 0; x < n_jobs; ++x) {
+    usp_rope_job j = jobs[x];
+    if (B == 1) j.s_b = j.d_b = 0;  // a stride of one step says nothing
+    if (S == 1) j.s_t = j.d_t = 0;
+    if (j.H == 1) j.s_h = j.d_h = 0;
+    if (!j.src || !j.dst) return record_error(USP_ERR_INVALID_ARG, "job %d: null pointer", x);
+    if (j.H <= 0) return record_error(USP_ERR_INVALID_ARG, "job %d: heads must be positive", x);
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(j.src) | reinterpret_cast<uintptr_t>(j.dst);
+    if (bits % es) return record_error(USP_ERR_INVALID_ARG, "job %d: misaligned pointer", x);
+    wide = wide && bits % 16 == 0;
+    const long long strides[6] = {j.s_b, j.s_t, j.s_h, j.d_b, j.d_t, j.d_h};
+    for (long long v : strides) {
+      if (v < 0) return record_error(USP_ERR_INVALID_ARG, "job %d: negative stride", x);
+      wide = wide && v % V == 0;
+    }
+    // two rows of the output must not share elements (an input may be broadcast by stride 0)
+    if ((B > 1 && j.d_b < D) || (S > 1 && j.d_t < D) || (j.H > 1 && j.d_h < D))
+      return record_error(USP_ERR_INVALID_ARG, "job %d: the output's rows overlap", x);
+    a.job[x].src = j.src;
+    a.job[x].dst = j.dst;
+    a.job[x].H = j.H;
+    a.job[x].s_b = j.s_b; a.job[x].s_t = j.s_t; a.job[x].s_h = j.s_h;
+    a.job[x].d_b = j.d_b; a.job[x].d_t = j.d_t; a.job[x].d_h = j.d_h;
+  }
+  a.n_jobs = n_jobs;
+  a.S = S; a.D = D; a.R = R;
+  a.pos = positions;
+  a.pos64 = pos_bits == 64;
+  a.inverse = inverse;
+  const long long tokens = static_cast<long long>(B) * S;
+  a.axis_step = tokens;
+  for (int f = 0; f < R / 2; ++f) {
+    if (!isfinite(inv_freq[f])) return record_error(USP_ERR_INVALID_ARG, "inv_freq[%d] is not finite", f);
+    if (axis[f] < 0 || axis[f] >= n_axes) return record_error(USP_ERR_INVALID_ARG, "axis[%d] = %d is outside 0..%d", f, axis[f], n_axes - 1);
+    const long double turns = static_cast<long double>(inv_freq[f]) / (2 * 3.14159265358979323846264338327950288L);
+    const long double frac = turns - floorl(turns);  // [0, 1): whole turns per position step do nothing
+    a.turn[f] = frac >= 1.0L ? 0ull : static_cast<unsigned long long>(frac * 18446744073709551616.0L);
+    a.axis[f] = static_cast<unsigned char>(axis[f]);
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (dtype == USP_BF16) {
+    e = wide ? (paired ? launch<__nv_bfloat16, 8, true>(a, tokens, st) : launch<__nv_bfloat16, 8, false>(a, tokens, st))
+             : (paired ? launch<__nv_bfloat16, 1, true>(a, tokens, st) : launch<__nv_bfloat16, 1, false>(a, tokens, st));
+  } else {
+    e = wide ? (paired ? launch<float, 4, true>(a, tokens, st) : launch<float, 4, false>(a, tokens, st))
+             : (paired ? launch<float, 1, true>(a, tokens, st) : launch<float, 1, false>(a, tokens, st));
+  }
+  return e == cudaSuccess ? USP_OK : record_error(USP_ERR_CUDA, "rotary positions launch: %s", cudaGetErrorString(e));
+}

@@ -1,0 +1,422 @@
+// usp_window_dq.cu -- backward of sliding-window attention with sinks, the
+// query-major half (dQ) on sm_100a:
+//   dQ_i = scale sum_j P_ij (dO_i.v_j - Delta_i) k_j
+// over the key tiles that the forward walks (usp_window.cuh). dQ accumulates in
+// TMEM over the walk and is written once, as bf16.
+//
+// A persistent CTA (one per SM, 320 threads) takes work items: one 128-row query
+// tile of one head.
+//   warp 0      TMA producer: Q, dO per item, K (3 stages) and V (2 stages) per key tile
+//   warp 1      UMMA issuer: S = Q K^T (two buffers), dP = dO V^T, dQ += dS K
+//   warps 2..9  two warpgroups of 64 key columns; thread = query row
+// TMEM: S / dS at 0 and 128, dP at 256, dQ at 384. The key tiles of all items of
+// a CTA form one stream: S runs two tiles and dP one tile ahead, into the next
+// item, whose first dQ product waits for dS, written by the warps that read this
+// item's dQ before it.
+#include <math.h>
+
+#include "usp_ptx.cuh"
+#include "usp_window.cuh"
+
+namespace usp {
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kComputeWarps = 8;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColDP = 256, kColDQ = 384;
+__host__ __device__ constexpr uint32_t col_s(int b) { return 128u * b; }
+
+template <int D>
+struct Cfg {
+  static constexpr int kPanels = D / 64;
+  static constexpr int kPanelBytes = 128 * 128;
+  static constexpr int kTileBytes = kPanels * kPanelBytes;
+  static constexpr int kKSt = 3;
+  static constexpr int kVSt = 2;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffDO = kTileBytes;
+  static constexpr int kOffK = 2 * kTileBytes;
+  static constexpr int kOffV = kOffK + kKSt * kTileBytes;
+  static constexpr int kOffBar = kOffV + kVSt * kTileBytes;
+  static constexpr int kSmemBytes = kOffBar + 256;
+};
+
+struct Args {
+  WinGeo g;
+  const float* lse2;
+  const float* delta;
+  int Lp;
+  __nv_bfloat16* dq;
+  int n_items;
+  int* status;
+  unsigned long long wait_ns;
+};
+
+struct Bars {
+  uint64_t q_full, q_empty, do_full, do_empty;
+  uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
+  uint64_t s_full[2], dp_full, dp_free, ds_full, dq_done[2], drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+enum : int {
+  kSiteQEmpty = 0x601, kSiteDoEmpty = 0x602, kSiteKEmpty = 0x603, kSiteVEmpty = 0x604, kSiteQ = 0x611, kSiteDo = 0x612,
+  kSiteK = 0x613, kSiteV = 0x614, kSiteDpFree = 0x615, kSiteDs = 0x616, kSiteDqDone = 0x617, kSiteS = 0x621,
+  kSiteDp = 0x622, kSiteEpi = 0x623, kSiteAlign = 0x6FF
+};
+
+struct Item {
+  int b, h, q0;
+};
+__device__ __forceinline__ Item item_of(const WinGeo& g, int idx) {
+  Item x;
+  x.q0 = (g.n_tiles - 1 - idx % g.n_tiles) * kBM;  // the causally heaviest first
+  idx /= g.n_tiles;
+  x.h = idx % g.Hq;
+  x.b = idx / g.Hq;
+  return x;
+}
+__device__ __forceinline__ KeyRun run_of(const WinGeo& g, const Item& x) {
+  return key_run(g, x.q0, min(x.q0 + kBM, g.S));
+}
+
+// A key tile of the CTA's stream: which of which item, and where its barriers stand.
+struct Cursor {
+  int idx, it, nt, item, n;  // work item, tile in it, its tiles, item and tile of the stream
+  __device__ __forceinline__ bool last() const { return it + 1 == nt; }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                     const Args a) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_addr(smem) & 1023u) {  // the swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) atomicCAS(a.status, 0, kSiteAlign);
+    return;
+  }
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::kOffBar);
+  static_assert(sizeof(Bars) <= 256, "barrier block");
+  uint8_t* sQ = smem + C::kOffQ;
+  uint8_t* sDO = smem + C::kOffDO;
+  uint8_t* sK = smem + C::kOffK;
+  uint8_t* sV = smem + C::kOffV;
+  const WinGeo& g = a.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int stride = gridDim.x;
+
+  if (threadIdx.x == 0) {
+    bars->abort_flag = *reinterpret_cast<volatile int*>(a.status) != 0;
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
+    mbar_init(&bars->do_full, 1);
+    mbar_init(&bars->do_empty, 1);
+    for (int s = 0; s < C::kKSt; ++s) {
+      mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->k_empty[s], 1);
+    }
+    for (int s = 0; s < C::kVSt; ++s) {
+      mbar_init(&bars->v_full[s], 1);
+      mbar_init(&bars->v_empty[s], 1);
+      mbar_init(&bars->s_full[s], 1);
+      mbar_init(&bars->dq_done[s], 1);
+    }
+    mbar_init(&bars->dp_full, 1);
+    mbar_init(&bars->dp_free, kComputeWarps);
+    mbar_init(&bars->ds_full, kComputeWarps);
+    mbar_init(&bars->drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(&bars->tmem_base, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  const WaitCtl w{&bars->abort_flag, a.status, a.wait_ns};
+  const bool skip = bars->abort_flag != 0;
+
+  if (skip) {
+    // nothing issued, nothing to drain
+  } else if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+      tma_prefetch_desc(&tm_do);
+    }
+    __syncwarp();
+    int nk = 0, nv = 0, n_q = 0, n_do = 0;
+    bool ok = true;
+    auto panels = [&](const CUtensorMap* tm, uint64_t* bar, uint8_t* dst, int head, int row, int b) {
+      mbar_expect_tx_w(bar, C::kTileBytes);
+      for (int p = 0; p < C::kPanels; ++p) tma_load_4d_w(tm, bar, dst + p * C::kPanelBytes, p * 64, head, row, b);
+    };
+    for (int idx = blockIdx.x; ok && idx < a.n_items; idx += stride) {
+      const Item x = item_of(g, idx);
+      const KeyRun kr = run_of(g, x);
+      const int kvh = x.h / g.G;
+      for (int it = 0; it < kr.nt; ++it) {
+        const int sk = nk % C::kKSt, sv = nv % C::kVSt;
+        if (nk >= C::kKSt && !mbar_wait_w(&bars->k_empty[sk], ((nk / C::kKSt) - 1) & 1, w, kSiteKEmpty)) { ok = false; break; }
+        panels(&tm_k, &bars->k_full[sk], sK + sk * C::kTileBytes, kvh, kr.tile(it) * kBN, x.b);
+        ++nk;
+        if (it == 0) {  // Q behind the first K, dO behind it: in the order in which their buffers free
+          if (n_q >= 1 && !mbar_wait_w(&bars->q_empty, (n_q - 1) & 1, w, kSiteQEmpty)) { ok = false; break; }
+          panels(&tm_q, &bars->q_full, sQ, x.h, x.q0, x.b);
+          ++n_q;
+          if (n_do >= 1 && !mbar_wait_w(&bars->do_empty, (n_do - 1) & 1, w, kSiteDoEmpty)) { ok = false; break; }
+          panels(&tm_do, &bars->do_full, sDO, x.h, x.q0, x.b);
+          ++n_do;
+        }
+        if (nv >= C::kVSt && !mbar_wait_w(&bars->v_empty[sv], ((nv / C::kVSt) - 1) & 1, w, kSiteVEmpty)) { ok = false; break; }
+        panels(&tm_v, &bars->v_full[sv], sV + sv * C::kTileBytes, kvh, kr.tile(it) * kBN, x.b);
+        ++nv;
+      }
+    }
+    if (*reinterpret_cast<volatile int*>(&bars->abort_flag)) {
+      if (n_q > 0) mbar_wait_drain(&bars->q_full, (n_q - 1) & 1, a.wait_ns);
+      if (n_do > 0) mbar_wait_drain(&bars->do_full, (n_do - 1) & 1, a.wait_ns);
+      for (int it = nk - C::kKSt < 0 ? 0 : nk - C::kKSt; it < nk; ++it)
+        mbar_wait_drain(&bars->k_full[it % C::kKSt], (it / C::kKSt) & 1, a.wait_ns);
+      for (int it = nv - C::kVSt < 0 ? 0 : nv - C::kVSt; it < nv; ++it)
+        mbar_wait_drain(&bars->v_full[it % C::kVSt], (it / C::kVSt) & 1, a.wait_ns);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ UMMA issuer
+    constexpr uint32_t kIdSS = idesc_bf16_f32(128, 128, 0, 0);
+    constexpr uint32_t kIdKM = idesc_bf16_f32(128, D, 0, 1);
+    const uint64_t dQ0 = sdesc_sw128(smem_addr(sQ), 16, 1024), dDO0 = sdesc_sw128(smem_addr(sDO), 16, 1024);
+    const uint64_t dK0 = sdesc_sw128(smem_addr(sK), 16, 1024), dV0 = sdesc_sw128(smem_addr(sV), 16, 1024);
+    const uint64_t dKmn = sdesc_sw128(smem_addr(sK), C::kPanelBytes, 1024);
+    bool issued_any = false;
+    auto tiles_of = [&](int idx) { return run_of(g, item_of(g, idx)).nt; };
+    auto next = [&](const Cursor& c) -> Cursor {  // the tile behind c (idx >= n_items: none)
+      Cursor x = c;
+      ++x.n;
+      if (c.last()) {
+        x.idx += stride;
+        x.it = 0;
+        ++x.item;
+        x.nt = x.idx < a.n_items ? tiles_of(x.idx) : 0;
+      } else {
+        ++x.it;
+      }
+      return x;
+    };
+    auto issue_s = [&](const Cursor& c) -> bool {  // S into buffer n & 1
+      if (c.it == 0 && !mbar_wait_w(&bars->q_full, c.item & 1, w, kSiteQ)) return false;
+      if (!mbar_wait_w(&bars->k_full[c.n % C::kKSt], (c.n / C::kKSt) & 1, w, kSiteK)) return false;
+      // dQ two tiles back has read its dS from the buffer
+      if (c.n >= 2 && !mbar_wait_w(&bars->dq_done[c.n & 1], ((c.n - 2) >> 1) & 1, w, kSiteDqDone)) return false;
+      tc_fence_after();
+      const uint64_t kd = dK0 + (((c.n % C::kKSt) * C::kTileBytes) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk >> 2) * C::kPanelBytes + (kk & 3) * 32) >> 4;
+        umma_bf16_w(tmem + col_s(c.n & 1), dQ0 + off, kd + off, kIdSS, kk > 0 ? 1u : 0u);
+      }
+      umma_commit_w(&bars->s_full[c.n & 1]);
+      if (c.last()) umma_commit_w(&bars->q_empty);
+      issued_any = true;
+      return true;
+    };
+    auto issue_dp = [&](const Cursor& c) -> bool {  // dP = dO V^T, once the previous dP has been read
+      if (c.it == 0 && !mbar_wait_w(&bars->do_full, c.item & 1, w, kSiteDo)) return false;
+      if (!mbar_wait_w(&bars->v_full[c.n % C::kVSt], (c.n / C::kVSt) & 1, w, kSiteV)) return false;
+      if (c.n >= 1 && !mbar_wait_w(&bars->dp_free, (c.n - 1) & 1, w, kSiteDpFree)) return false;
+      tc_fence_after();
+      const uint64_t vd = dV0 + (((c.n % C::kVSt) * C::kTileBytes) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk >> 2) * C::kPanelBytes + (kk & 3) * 32) >> 4;
+        umma_bf16_w(tmem + kColDP, dDO0 + off, vd + off, kIdSS, kk > 0 ? 1u : 0u);
+      }
+      umma_commit_w(&bars->dp_full);
+      umma_commit_w(&bars->v_empty[c.n % C::kVSt]);
+      if (c.last()) umma_commit_w(&bars->do_empty);
+      return true;
+    };
+    auto issue_dq = [&](const Cursor& c) -> bool {  // dQ += dS K
+      if (!mbar_wait_w(&bars->ds_full, c.n & 1, w, kSiteDs)) return false;
+      tc_fence_after();
+      const uint64_t kd = dKmn + (((c.n % C::kKSt) * C::kTileBytes) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < kBN / 16; ++kk) {
+        const uint32_t pcol = col_s(c.n & 1) + (kk < 4 ? 0u : 64u) + (kk & 3) * 8;
+        umma_bf16_tmem_a_w(tmem + kColDQ, tmem + pcol, kd + ((kk * 16 * 128) >> 4), kIdKM,
+                           (c.it > 0 || kk > 0) ? 1u : 0u);
+      }
+      umma_commit_w(&bars->dq_done[c.n & 1]);
+      umma_commit_w(&bars->k_empty[c.n % C::kKSt]);
+      return true;
+    };
+    bool ok = true;
+    Cursor c{static_cast<int>(blockIdx.x), 0, 0, 0, 0};
+    if (c.idx < a.n_items) {
+      c.nt = tiles_of(c.idx);
+      Cursor c1 = next(c);
+      ok = issue_s(c) && issue_dp(c);
+      // (S of a second tile only inside the item: the next item's Q shares this one's buffer)
+      bool s1_done = ok && c1.idx < a.n_items && c1.it > 0;
+      if (s1_done) ok = issue_s(c1);
+      while (ok) {
+        const bool more = c1.idx < a.n_items;
+        if (more && c1.it > 0) {
+          // dP of the next tile as soon as this one's has been read, ahead of dQ
+          ok = issue_dp(c1) && issue_dq(c);
+        } else {
+          ok = issue_dq(c);  // the next item's dO may still be on its way
+          if (ok && more) ok = (s1_done || issue_s(c1)) && issue_dp(c1);
+          s1_done = true;
+        }
+        if (!ok || !more) break;
+        const Cursor c2 = next(c1);  // S two tiles ahead
+        s1_done = c2.idx < a.n_items && c2.it > 0;
+        if (s1_done) ok = issue_s(c2);
+        c = c1;
+        c1 = c2;
+      }
+    }
+    if (!ok && issued_any) {
+      umma_commit_w(&bars->drain);
+      mbar_wait_drain(&bars->drain, 0, a.wait_ns);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ compute warps
+    const int wg = (warp - 2) >> 2;  // key columns [64 wg, 64 wg + 64)
+    const int wq = warp & 3;
+    const int row = wq * 32 + lane;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+    const int cbase = wg * 64;
+    const float2 sl2 = make_float2(g.scale_log2, g.scale_log2);
+    bool ok = true;
+    int n = 0;
+    for (int idx = blockIdx.x; ok && idx < a.n_items; idx += stride) {
+      const Item x = item_of(g, idx);
+      const KeyRun kr = run_of(g, x);
+      const int i = x.q0 + row;
+      const bool store = i < g.S;
+      const size_t tab = (static_cast<size_t>(x.b) * g.Hq + x.h) * a.Lp + i;  // Lp covers the whole tile
+      const float nl = __ldg(a.lse2 + tab);  // -inf on padding rows: their P is 0
+      const float nd = __ldg(a.delta + tab);
+      const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
+      int lo = 0, first = INT_MAX, sink_end = 0;
+      if (store) {
+        lo = win_lo(g, i);
+        first = max(lo, i - g.W + 1);
+        sink_end = min(lo + g.ns, i + 1);
+      }
+      const int q_last = min(x.q0 + kBM, g.S) - 1;
+      const int first_all = max(win_lo(g, q_last), q_last - g.W + 1);
+      for (int it = 0; it < kr.nt; ++it, ++n) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[n & 1], (n >> 1) & 1, w, kSiteS));
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->dp_full, n & 1, w, kSiteDp));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t cS = col_s(n & 1);
+        const int k0 = kr.tile(it) * kBN;
+        const bool whole = k0 >= first_all && k0 + kBN - 1 <= x.q0;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int c0 = cbase + half * 32;
+          uint32_t rs[32], rp[32];
+          tmem_ld32(trow + cS + c0, rs);
+          tmem_ld32(trow + kColDP + c0, rp);
+          tmem_ld_wait();
+          reg_fence32(rs);
+          reg_fence32(rp);
+          if (half == 1) {  // every dP column of this thread has been read
+            tc_fence_before();
+            mbar_arrive_warp(&bars->dp_free);
+          }
+          if (!whole) {
+            const uint32_t vis = bits_between(first - k0, i + 1 - k0, c0) | bits_between(lo - k0, sink_end - k0, c0);
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((vis >> c) & 1u)) rs[c] = 0xFF800000u;
+          }
+          uint32_t dk[16];
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float2 y = ffma2(make_float2(__uint_as_float(rs[c]), __uint_as_float(rs[c + 1])), sl2, nl2);
+            const float2 pv = make_float2(ex2_approx(y.x), ex2_approx(y.y));  // -inf -> 0
+            const float2 ds = fmul2(pv, fadd2(make_float2(__uint_as_float(rp[c]), __uint_as_float(rp[c + 1])), nd2));
+            dk[c >> 1] = pack_bf16x2(ds.x, ds.y);
+          }
+          tmem_st16(trow + cS + cbase + half * 16, dk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(&bars->ds_full);
+      }
+      // ------------------------------------------------------------ epilogue: dQ rows
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->dq_done[(n - 1) & 1], ((n - 1) >> 1) & 1, w, kSiteEpi));
+      if (ok) {
+        tc_fence_after();
+        const size_t qr = (static_cast<size_t>(x.b) * g.S + (store ? i : 0)) * g.Hq + x.h;
+#pragma unroll
+        for (int c0 = wg * (D / 2); c0 < (wg + 1) * (D / 2); c0 += 32) {
+          uint32_t o[32];
+          tmem_ld32(trow + kColDQ + c0, o);
+          tmem_ld_wait();
+          reg_fence32(o);
+          if (store) {
+            uint4* dst = reinterpret_cast<uint4*>(a.dq + qr * D + c0);
+            auto pk = [&](int c) {
+              return pack_bf16x2(__uint_as_float(o[c]) * g.scale, __uint_as_float(o[c + 1]) * g.scale);
+            };
+#pragma unroll
+            for (int q = 0; q < 4; ++q) dst[q] = make_uint4(pk(q * 8), pk(q * 8 + 2), pk(q * 8 + 4), pk(q * 8 + 6));
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const WinLaunch& L, cudaStream_t stream) {
+  using C = Cfg<D>;
+  static_assert(C::kSmemBytes <= 227 * 1024, "shared memory budget");
+  cudaError_t e =
+      cudaFuncSetAttribute(window_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  Args a{};
+  a.g = L.g;
+  a.lse2 = L.lse2;
+  a.delta = L.delta;
+  a.Lp = L.Lp;
+  a.dq = static_cast<__nv_bfloat16*>(L.dq);
+  a.status = L.status;
+  a.wait_ns = L.wait_ns;
+  const long long items = static_cast<long long>(L.g.n_tiles) * L.g.Hq * L.g.B;
+  if (items > 0x3FFFFFFFLL) return cudaErrorInvalidConfiguration;
+  a.n_items = static_cast<int>(items);
+  const int sms = sm_count();
+  const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);
+  window_dq_kernel<D><<<grid, kThreads, C::kSmemBytes, stream>>>(L.tm_q, L.tm_k, L.tm_v, L.tm_do, a);
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_window_dq(const WinLaunch& L, cudaStream_t stream) {
+  return L.D == 128 ? launch_d<128>(L, stream) : L.D == 64 ? launch_d<64>(L, stream) : cudaErrorInvalidValue;
+}
+
+}  // namespace usp
