@@ -4,6 +4,9 @@ the path happens here.
 """
 from __future__ import annotations
 
+import contextlib
+import functools
+
 import torch
 
 from . import binding as B_
@@ -271,6 +274,9 @@ def bwd_preprocess(out: torch.Tensor, dO: torch.Tensor, stream=None) -> torch.Te
     return delta
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _check(name: str, t: torch.Tensor, ref: torch.Tensor, dtype, shape=None, contiguous=True) -> torch.Tensor:
     """An argument of the calls below: a tensor of ref's device with this type and shape."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != ref.device:
@@ -284,43 +290,33 @@ def _check(name: str, t: torch.Tensor, ref: torch.Tensor, dtype, shape=None, con
     return t
 
 
-class _on:
-    """The device of `ref` and the stream that a call runs on: ref's device's current stream, or
-    the given one. What the call allocates inside belongs to that stream, and the inputs are kept
+def _on(ref: torch.Tensor, stream, *inputs):
+    """(context, raw stream) of a call: the current stream of ref's device, or the given one. What the
+    call allocates inside the context belongs to that stream; with a given stream the inputs are kept
     from the allocator until its work on them is done."""
-
-    def __init__(self, ref: torch.Tensor, stream, *inputs):
-        self.ctx = None
-        if stream is not None:
-            s = torch.cuda.ExternalStream(stream, ref.device) if isinstance(stream, int) else stream
-            if s.device != ref.device:
-                raise ValueError("the stream is of another device than the tensors")
-            for t in inputs:
-                if t is not None:
-                    t.record_stream(s)
-            self.ctx = torch.cuda.stream(s)
-        elif ref.device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(ref.device)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *a):
-        if self.ctx is not None:
-            self.ctx.__exit__(*a)
+    index = ref.device.index
+    if stream is not None:
+        s = torch.cuda.ExternalStream(stream, ref.device) if isinstance(stream, int) else stream
+        if s.device != ref.device:
+            raise ValueError("the stream is of another device than the tensors")
+        for t in inputs:
+            if t is not None:
+                t.record_stream(s)
+        return torch.cuda.stream(s), s.cuda_stream
+    # (torch.cuda.current_stream() builds an object at ten times the price)
+    return (_HERE if index == torch._C._cuda_getDevice() else torch.cuda.device(ref.device),
+            torch._C._cuda_getCurrentRawStream(index))
 
 
 def _scratch(ws, nbytes: int, ref: torch.Tensor) -> torch.Tensor:
     """The given workspace, or a new one (the calls below clear what they need of it)."""
     if ws is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=ref.device)
+        return ref.new_empty(nbytes, dtype=torch.uint8)
     return _check("ws", ws, ref, torch.uint8)
 
 
 def _new(t, name: str, shape, dtype, ref: torch.Tensor) -> torch.Tensor:
-    return torch.empty(shape, dtype=dtype, device=ref.device) if t is None else _check(name, t, ref, dtype, shape)
+    return ref.new_empty(shape, dtype=dtype) if t is None else _check(name, t, ref, dtype, shape)
 
 
 def _window_geometry(q, k, v, window, sinks, cu_seqlens):
@@ -340,6 +336,16 @@ def _window_geometry(q, k, v, window, sinks, cu_seqlens):
     return (B, S, Hq, Hkv, D, int(window), int(sinks)), n_docs
 
 
+@functools.lru_cache(maxsize=256)
+def _window_ws(*geometry) -> int:
+    return _ws_bytes(B_.usp_window_workspace_size(*geometry), "window attention", *geometry)
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_ws(*geometry) -> int:
+    return _ws_bytes(B_.usp_window_decode_workspace_size(*geometry), "window decode", *geometry)
+
+
 def _ws_bytes(n: int, what: str, *geometry) -> int:
     if n == 0:
         raise B_.UspError(B_.USP_ERR_UNSUPPORTED, f"{what}{geometry}: {B_.usp_last_error()}")
@@ -353,8 +359,9 @@ def window_attn_fwd(q, k, v, window: int, sinks: int = 0, cu_seqlens=None, ws=No
     `sinks` keys; with cu_seqlens ([n_docs + 1] int32, CUDA) all within its document. Returns
     (out bf16 like q, lse fp32 [B, S, Hq]). Elements must be finite, hidden ones too."""
     geo, n_docs = _window_geometry(q, k, v, window, sinks, cu_seqlens)
-    need = _ws_bytes(B_.usp_window_workspace_size(*geo, n_docs, 0), "window attention", *geo)
-    with _on(q, stream, q, k, v, cu_seqlens, ws, out, lse) as st:
+    need = _window_ws(*geo, n_docs, 0)
+    ctx, st = _on(q, stream, q, k, v, cu_seqlens, ws, out, lse)
+    with ctx:
         out = _new(out, "out", q.shape, torch.bfloat16, q)
         lse = _new(lse, "lse", q.shape[:-1], torch.float32, q)
         ws = _scratch(ws, need, q)
@@ -371,8 +378,9 @@ def window_attn_bwd(q, k, v, out, lse, dO, window: int, sinks: int = 0, cu_seqle
     _check("out", out, q, torch.bfloat16, q.shape)
     _check("dO", dO, q, torch.bfloat16, q.shape)
     _check("lse", lse, q, torch.float32, q.shape[:-1])
-    need = _ws_bytes(B_.usp_window_workspace_size(*geo, n_docs, 1), "window attention", *geo)
-    with _on(q, stream, q, k, v, out, lse, dO, cu_seqlens, ws, dq, dk, dv) as st:
+    need = _window_ws(*geo, n_docs, 1)
+    ctx, st = _on(q, stream, q, k, v, out, lse, dO, cu_seqlens, ws, dq, dk, dv)
+    with ctx:
         dq = _new(dq, "dq", q.shape, torch.bfloat16, q)
         dk = _new(dk, "dk", k.shape, torch.bfloat16, q)
         dv = _new(dv, "dv", v.shape, torch.bfloat16, q)
@@ -402,8 +410,9 @@ def window_attn_decode(q, k_cache, v_cache, lens, window: int, sinks: int = 0, w
     if ks[3] != 1 or vs[3] != 1:
         raise ValueError("the last dimension of the caches must be contiguous")
     geo = (N, n, cap, Hq, Hkv, D, int(window), int(sinks))
-    need = _ws_bytes(B_.usp_window_decode_workspace_size(*geo), "window decode", *geo)
-    with _on(q, stream, q, k_cache, v_cache, lens, ws, out, lse) as st:
+    need = _decode_ws(*geo)
+    ctx, st = _on(q, stream, q, k_cache, v_cache, lens, ws, out, lse)
+    with ctx:
         out = _new(out, "out", q.shape, torch.bfloat16, q)
         lse = _new(lse, "lse", q.shape[:-1], torch.float32, q)
         ws = _scratch(ws, need, q)
@@ -445,7 +454,8 @@ def rope_axes(xs, positions, inv_freq, axis, paired: bool = False, inverse: bool
     outs = ((outs,) if single else tuple(outs)) if outs is not None else (None,) * len(xs)
     if len(outs) != len(xs):
         raise ValueError("one output per tensor")
-    with _on(x0, stream, positions, *xs, *outs) as st:
+    ctx, st = _on(x0, stream, positions, *xs, *outs)
+    with ctx:
         ys, jobs = [], []
         for x, y in zip(xs, outs):
             y = (torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None

@@ -336,9 +336,7 @@ def usp_rope_axes(jobs, B, S, D, R, dtype, positions, pos_bits, n_axes, inv_freq
                   check=True):
     """jobs: sequence of (src, dst, H, (s_b, s_t, s_h), (d_b, d_t, d_h)); inv_freq (float64) and axis (int32) in
     host memory: CPU tensors or addresses."""
-    arr = (RopeJob * max(len(jobs), 1))()
-    for x, (src, dst, H, ss, ds) in enumerate(jobs):
-        arr[x] = RopeJob(_ptr(src), _ptr(dst), H, *ss, *ds)
+    arr = (RopeJob * max(len(jobs), 1))(*[(_ptr(src), _ptr(dst), H, *ss, *ds) for src, dst, H, ss, ds in jobs])
     rc = lib().usp_rope_axes(arr, len(jobs), B, S, D, R, dtype, _ptr(positions), pos_bits, n_axes, _ptr(inv_freq),
                              _ptr(axis), int(paired), int(inverse), _stream(stream))
     return _check(rc) if check else rc

@@ -228,7 +228,7 @@ struct WinLaunch {
   void* out;
   float* lse;
   void *dq, *dk, *dv;          // bf16
-  const float *lse2, *delta;   // [B*Hq][Lp]: -LSE*log2(e), -Delta (launch_bwd_prep_rows)
+  float *lse2, *delta;         // [B*Hq][Lp]: -LSE*log2(e), -Delta; -inf and 0 on padding rows
   int Lp;
   const void *q, *k, *v, *dO;  // the tensors behind the maps (far sinks)
   float* far_part;             // [B][Hkv][n_tiles][ns][2][D]
@@ -237,8 +237,11 @@ struct WinLaunch {
   unsigned long long wait_ns;
 };
 cudaError_t launch_window_fwd(const WinLaunch& L, cudaStream_t stream);
-cudaError_t launch_window_dkdv(const WinLaunch& L, cudaStream_t stream);
+// The backward's launches in their order: the row tables; dQ, which corrects the
+// Delta table; the sinks' far sums; dK and dV.
+cudaError_t launch_window_prep(const WinLaunch& L, const void* out, const float* lse, cudaStream_t stream);
 cudaError_t launch_window_dq(const WinLaunch& L, cudaStream_t stream);
+cudaError_t launch_window_dkdv(const WinLaunch& L, cudaStream_t stream);
 // dK, dV of the sinks from the queries outside their key tile's band: far_part, then far_sum.
 cudaError_t launch_window_far(const WinLaunch& L, cudaStream_t stream);
 

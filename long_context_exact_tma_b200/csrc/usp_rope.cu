@@ -236,8 +236,9 @@ extern "C" int usp_rope_axes(const usp_rope_job* jobs, int n_jobs, int B, int S,
   for (int f = 0; f < R / 2; ++f) {
     if (!isfinite(inv_freq[f])) return record_error(USP_ERR_INVALID_ARG, "inv_freq[%d] is not finite", f);
     if (axis[f] < 0 || axis[f] >= n_axes) return record_error(USP_ERR_INVALID_ARG, "axis[%d] = %d is outside 0..%d", f, axis[f], n_axes - 1);
-    const long double turns = static_cast<long double>(inv_freq[f]) / (2 * 3.14159265358979323846264338327950288L);
-    const long double frac = turns - floorl(turns);  // [0, 1): whole turns per position step do nothing
+    const long double turns = static_cast<long double>(inv_freq[f]) * 0.159154943091895335768883763372514362L;
+    // [0, 1): whole turns per position step do nothing
+    const long double frac = turns >= 0.0L && turns < 1.0L ? turns : turns - floorl(turns);
     a.turn[f] = frac >= 1.0L ? 0ull : static_cast<unsigned long long>(frac * 18446744073709551616.0L);
     a.axis[f] = static_cast<unsigned char>(axis[f]);
   }

@@ -1,6 +1,6 @@
 // usp_window.cu -- entry points of causal attention with a sliding window and
-// sinks over [B][S][H][D] (kernels: usp_window_fwd.cu, usp_window_bwd.cu,
-// usp_window_dq.cu, usp_window_sink.cu).
+// sinks over [B][S][H][D] (kernels: usp_window_fwd.cu, usp_window_prep.cu,
+// usp_window_dq.cu, usp_window_sink.cu, usp_window_bwd.cu).
 #include <math.h>
 
 #include "../../include/usp.h"
@@ -132,9 +132,9 @@ extern "C" int usp_window_attn_bwd(const void* q, const void* k, const void* v, 
   L.status = static_cast<int*>(workspace);
   L.wait_ns = current_wait_ns();
   cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(int), st);
-  if (e == cudaSuccess) e = launch_bwd_prep_rows(out, dO, lse, delta, lse2, B, S, Hq, D, L.Lp, st);
+  if (e == cudaSuccess) e = launch_window_prep(L, out, lse, st);
+  if (e == cudaSuccess) e = launch_window_dq(L, st);
   if (e == cudaSuccess && L.far_sum) e = launch_window_far(L, st);
   if (e == cudaSuccess) e = launch_window_dkdv(L, st);
-  if (e == cudaSuccess) e = launch_window_dq(L, st);
   return e == cudaSuccess ? USP_OK : record_error(USP_ERR_CUDA, "window attention backward: %s", cudaGetErrorString(e));
 }

@@ -9,6 +9,15 @@
 //   warp 0      TMA producer: Q, dO per item, K (3 stages) and V (2 stages) per key tile
 //   warp 1      UMMA issuer: S = Q K^T (two buffers), dP = dO V^T, dQ += dS K
 //   warps 2..9  two warpgroups of 64 key columns; thread = query row
+// The gradient sums of a row cancel: sum_j dS_ij = 0 with the exact Delta_i =
+// sum_j P_ij dP_ij, while dO.O of the bf16 output is off by up to 2^-8 |dO||O|. The
+// kernel adds up the residue r_i = sum_j dS_ij in fp32 and writes Delta_i + r_i back
+// to the table, for the key-major kernels that run after it. Its own sum is off by
+// r_i sum_j P_ij k_j, which matters next to dQ's own rounding only where few keys
+// share a row's weight (the ratio falls with the root of their number: 1.2 of the
+// rounding at 4 keys, 0.4 at 64): query tiles with rows of fewer than 48 keys walk
+// their key tiles twice, the second time with dS = -r_i P_ij.
+//
 // TMEM: S / dS at 0 and 128, dP at 256, dQ at 384. The key tiles of all items of
 // a CTA form one stream: S runs two tiles and dP one tile ahead, into the next
 // item, whose first dQ product waits for dS, written by the warps that read this
@@ -39,13 +48,14 @@ struct Cfg {
   static constexpr int kOffK = 2 * kTileBytes;
   static constexpr int kOffV = kOffK + kKSt * kTileBytes;
   static constexpr int kOffBar = kOffV + kVSt * kTileBytes;
-  static constexpr int kSmemBytes = kOffBar + 256;
+  static constexpr int kOffRes = kOffBar + 256;  // residues: [item parity][warpgroup][row]
+  static constexpr int kSmemBytes = kOffRes + 2 * 2 * 128 * 4;
 };
 
 struct Args {
   WinGeo g;
   const float* lse2;
-  const float* delta;
+  float* delta;
   int Lp;
   __nv_bfloat16* dq;
   int n_items;
@@ -57,6 +67,7 @@ struct Bars {
   uint64_t q_full, q_empty, do_full, do_empty;
   uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
   uint64_t s_full[2], dp_full, dp_free, ds_full, dq_done[2], drain;
+  uint64_t r_full;  // both warpgroups' residues of the item are in sRes
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -64,7 +75,7 @@ struct Bars {
 enum : int {
   kSiteQEmpty = 0x601, kSiteDoEmpty = 0x602, kSiteKEmpty = 0x603, kSiteVEmpty = 0x604, kSiteQ = 0x611, kSiteDo = 0x612,
   kSiteK = 0x613, kSiteV = 0x614, kSiteDpFree = 0x615, kSiteDs = 0x616, kSiteDqDone = 0x617, kSiteS = 0x621,
-  kSiteDp = 0x622, kSiteEpi = 0x623, kSiteAlign = 0x6FF
+  kSiteDp = 0x622, kSiteEpi = 0x623, kSiteRes = 0x624, kSiteAlign = 0x6FF
 };
 
 struct Item {
@@ -78,14 +89,30 @@ __device__ __forceinline__ Item item_of(const WinGeo& g, int idx) {
   x.b = idx / g.Hq;
   return x;
 }
-__device__ __forceinline__ KeyRun run_of(const WinGeo& g, const Item& x) {
-  return key_run(g, x.q0, min(x.q0 + kBM, g.S));
+// The item's key tiles, twice where a row has few keys.
+constexpr int kFewKeys = 48;
+struct DqRun {
+  KeyRun kr;
+  int n1, nt;  // tiles of one pass and of all
+  __device__ __forceinline__ int pass_it(int it) const { return it < n1 ? it : it - n1; }
+  __device__ __forceinline__ int base(int it) const { return kr.base(pass_it(it)); }
+  __device__ __forceinline__ int width(int it) const { return kr.width(pass_it(it)); }
+};
+__device__ __forceinline__ DqRun run_of(const WinGeo& g, const Item& x) {
+  DqRun r;
+  const int qe = min(x.q0 + kBM, g.S);
+  r.kr = key_run(g, x.q0, qe);
+  r.n1 = r.nt = r.kr.nt;
+  if (g.W + g.ns < kFewKeys || x.q0 - r.kr.lo + 1 < kFewKeys || win_lo(g, qe - 1) > x.q0) r.nt *= 2;
+  return r;
 }
 
 // A key tile of the CTA's stream: which of which item, and where its barriers stand.
 struct Cursor {
-  int idx, it, nt, item, n;  // work item, tile in it, its tiles, item and tile of the stream
-  __device__ __forceinline__ bool last() const { return it + 1 == nt; }
+  int idx, it, item, n;  // work item, tile in it, item and tile of the stream
+  DqRun run;
+  __device__ __forceinline__ bool last() const { return it + 1 == run.nt; }
+  __device__ __forceinline__ int width() const { return run.width(it); }
 };
 
 template <int D>
@@ -105,6 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sDO = smem + C::kOffDO;
   uint8_t* sK = smem + C::kOffK;
   uint8_t* sV = smem + C::kOffV;
+  float* sRes = reinterpret_cast<float*>(smem + C::kOffRes);
   const WinGeo& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stride = gridDim.x;
@@ -128,6 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars->dp_full, 1);
     mbar_init(&bars->dp_free, kComputeWarps);
     mbar_init(&bars->ds_full, kComputeWarps);
+    mbar_init(&bars->r_full, kComputeWarps);
     mbar_init(&bars->drain, 1);
     fence_mbar_init();
   }
@@ -158,12 +187,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (int idx = blockIdx.x; ok && idx < a.n_items; idx += stride) {
       const Item x = item_of(g, idx);
-      const KeyRun kr = run_of(g, x);
+      const DqRun kr = run_of(g, x);
       const int kvh = x.h / g.G;
       for (int it = 0; it < kr.nt; ++it) {
         const int sk = nk % C::kKSt, sv = nv % C::kVSt;
         if (nk >= C::kKSt && !mbar_wait_w(&bars->k_empty[sk], ((nk / C::kKSt) - 1) & 1, w, kSiteKEmpty)) { ok = false; break; }
-        panels(&tm_k, &bars->k_full[sk], sK + sk * C::kTileBytes, kvh, kr.tile(it) * kBN, x.b);
+        panels(&tm_k, &bars->k_full[sk], sK + sk * C::kTileBytes, kvh, kr.base(it), x.b);
         ++nk;
         if (it == 0) {  // Q behind the first K, dO behind it: in the order in which their buffers free
           if (n_q >= 1 && !mbar_wait_w(&bars->q_empty, (n_q - 1) & 1, w, kSiteQEmpty)) { ok = false; break; }
@@ -174,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++n_do;
         }
         if (nv >= C::kVSt && !mbar_wait_w(&bars->v_empty[sv], ((nv / C::kVSt) - 1) & 1, w, kSiteVEmpty)) { ok = false; break; }
-        panels(&tm_v, &bars->v_full[sv], sV + sv * C::kTileBytes, kvh, kr.tile(it) * kBN, x.b);
+        panels(&tm_v, &bars->v_full[sv], sV + sv * C::kTileBytes, kvh, kr.base(it), x.b);
         ++nv;
       }
     }
@@ -189,13 +218,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ UMMA issuer
-    constexpr uint32_t kIdSS = idesc_bf16_f32(128, 128, 0, 0);
     constexpr uint32_t kIdKM = idesc_bf16_f32(128, D, 0, 1);
     const uint64_t dQ0 = sdesc_sw128(smem_addr(sQ), 16, 1024), dDO0 = sdesc_sw128(smem_addr(sDO), 16, 1024);
     const uint64_t dK0 = sdesc_sw128(smem_addr(sK), 16, 1024), dV0 = sdesc_sw128(smem_addr(sV), 16, 1024);
     const uint64_t dKmn = sdesc_sw128(smem_addr(sK), C::kPanelBytes, 1024);
     bool issued_any = false;
-    auto tiles_of = [&](int idx) { return run_of(g, item_of(g, idx)).nt; };
     auto next = [&](const Cursor& c) -> Cursor {  // the tile behind c (idx >= n_items: none)
       Cursor x = c;
       ++x.n;
@@ -203,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         x.idx += stride;
         x.it = 0;
         ++x.item;
-        x.nt = x.idx < a.n_items ? tiles_of(x.idx) : 0;
+        if (x.idx < a.n_items) x.run = run_of(g, item_of(g, x.idx));
       } else {
         ++x.it;
       }
@@ -216,10 +243,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (c.n >= 2 && !mbar_wait_w(&bars->dq_done[c.n & 1], ((c.n - 2) >> 1) & 1, w, kSiteDqDone)) return false;
       tc_fence_after();
       const uint64_t kd = dK0 + (((c.n % C::kKSt) * C::kTileBytes) >> 4);
+      const uint32_t idesc = idesc_bf16_f32(128, c.width(), 0, 0);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = ((kk >> 2) * C::kPanelBytes + (kk & 3) * 32) >> 4;
-        umma_bf16_w(tmem + col_s(c.n & 1), dQ0 + off, kd + off, kIdSS, kk > 0 ? 1u : 0u);
+        umma_bf16_w(tmem + col_s(c.n & 1), dQ0 + off, kd + off, idesc, kk > 0 ? 1u : 0u);
       }
       umma_commit_w(&bars->s_full[c.n & 1]);
       if (c.last()) umma_commit_w(&bars->q_empty);
@@ -232,10 +260,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (c.n >= 1 && !mbar_wait_w(&bars->dp_free, (c.n - 1) & 1, w, kSiteDpFree)) return false;
       tc_fence_after();
       const uint64_t vd = dV0 + (((c.n % C::kVSt) * C::kTileBytes) >> 4);
+      const uint32_t idesc = idesc_bf16_f32(128, c.width(), 0, 0);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = ((kk >> 2) * C::kPanelBytes + (kk & 3) * 32) >> 4;
-        umma_bf16_w(tmem + kColDP, dDO0 + off, vd + off, kIdSS, kk > 0 ? 1u : 0u);
+        umma_bf16_w(tmem + kColDP, dDO0 + off, vd + off, idesc, kk > 0 ? 1u : 0u);
       }
       umma_commit_w(&bars->dp_full);
       umma_commit_w(&bars->v_empty[c.n % C::kVSt]);
@@ -246,8 +275,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mbar_wait_w(&bars->ds_full, c.n & 1, w, kSiteDs)) return false;
       tc_fence_after();
       const uint64_t kd = dKmn + (((c.n % C::kKSt) * C::kTileBytes) >> 4);
+      const int steps = c.width() / 16;  // 1, 2 or 8
 #pragma unroll
       for (int kk = 0; kk < kBN / 16; ++kk) {
+        if (kk >= steps) break;
         const uint32_t pcol = col_s(c.n & 1) + (kk < 4 ? 0u : 64u) + (kk & 3) * 8;
         umma_bf16_tmem_a_w(tmem + kColDQ, tmem + pcol, kd + ((kk * 16 * 128) >> 4), kIdKM,
                            (c.it > 0 || kk > 0) ? 1u : 0u);
@@ -257,9 +288,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     bool ok = true;
-    Cursor c{static_cast<int>(blockIdx.x), 0, 0, 0, 0};
+    Cursor c{static_cast<int>(blockIdx.x), 0, 0, 0, DqRun{}};
     if (c.idx < a.n_items) {
-      c.nt = tiles_of(c.idx);
+      c.run = run_of(g, item_of(g, c.idx));
       Cursor c1 = next(c);
       ok = issue_s(c) && issue_dp(c);
       // (S of a second tile only inside the item: the next item's Q shares this one's buffer)
@@ -297,65 +328,92 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cbase = wg * 64;
     const float2 sl2 = make_float2(g.scale_log2, g.scale_log2);
     bool ok = true;
-    int n = 0;
-    for (int idx = blockIdx.x; ok && idx < a.n_items; idx += stride) {
+    int n = 0, item = 0;
+    for (int idx = blockIdx.x; ok && idx < a.n_items; idx += stride, ++item) {
       const Item x = item_of(g, idx);
-      const KeyRun kr = run_of(g, x);
+      const DqRun kr = run_of(g, x);
       const int i = x.q0 + row;
       const bool store = i < g.S;
       const size_t tab = (static_cast<size_t>(x.b) * g.Hq + x.h) * a.Lp + i;  // Lp covers the whole tile
-      const float nl = __ldg(a.lse2 + tab);  // -inf on padding rows: their P is 0
-      const float nd = __ldg(a.delta + tab);
+      const float nl = a.lse2[tab];  // -inf on padding rows: their P is 0
+      const float nd = a.delta[tab];
       const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
-      int lo = 0, first = INT_MAX, sink_end = 0;
-      if (store) {
-        lo = win_lo(g, i);
-        first = max(lo, i - g.W + 1);
-        sink_end = min(lo + g.ns, i + 1);
-      }
+      const RowSpan span = row_span(g, i);
       const int q_last = min(x.q0 + kBM, g.S) - 1;
       const int first_all = max(win_lo(g, q_last), q_last - g.W + 1);
+      float2 res2 = make_float2(0.f, 0.f);
+      float res = 0.f;
       for (int it = 0; it < kr.nt; ++it, ++n) {
+        if (it == kr.n1) {  // the second pass needs the row's residue
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->r_full, item & 1, w, kSiteRes));
+          if (!ok) break;
+          const float* s = sRes + (item & 1) * 256 + row;
+          res = s[0] + s[128];
+        }
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[n & 1], (n >> 1) & 1, w, kSiteS));
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->dp_full, n & 1, w, kSiteDp));
         if (!ok) break;
         tc_fence_after();
         const uint32_t cS = col_s(n & 1);
-        const int k0 = kr.tile(it) * kBN;
+        const int k0 = kr.base(it), width = kr.width(it);
         const bool whole = k0 >= first_all && k0 + kBN - 1 <= x.q0;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int c0 = cbase + half * 32;
           uint32_t rs[32], rp[32];
-          tmem_ld32(trow + cS + c0, rs);
-          tmem_ld32(trow + kColDP + c0, rp);
-          tmem_ld_wait();
-          reg_fence32(rs);
-          reg_fence32(rp);
+          const bool used = c0 < width;  // a narrow tile has the first 32 columns at most
+          if (used) {
+            tmem_ld32(trow + cS + c0, rs);
+            tmem_ld32(trow + kColDP + c0, rp);
+            tmem_ld_wait();
+            reg_fence32(rs);
+            reg_fence32(rp);
+          }
           if (half == 1) {  // every dP column of this thread has been read
             tc_fence_before();
             mbar_arrive_warp(&bars->dp_free);
           }
+          if (!used) continue;
           if (!whole) {
-            const uint32_t vis = bits_between(first - k0, i + 1 - k0, c0) | bits_between(lo - k0, sink_end - k0, c0);
+            const uint32_t vis = visible_bits(span, kr.kr, kr.pass_it(it), k0, c0);
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-              if (!((vis >> c) & 1u)) rs[c] = 0xFF800000u;
+              if (!((vis >> c) & 1u)) {
+                rs[c] = 0xFF800000u;
+                rp[c] = 0u;  // columns past a narrow tile's width hold what an earlier tile left
+              }
           }
           uint32_t dk[16];
+          if (it < kr.n1) {
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float2 y = ffma2(make_float2(__uint_as_float(rs[c]), __uint_as_float(rs[c + 1])), sl2, nl2);
-            const float2 pv = make_float2(ex2_approx(y.x), ex2_approx(y.y));  // -inf -> 0
-            const float2 ds = fmul2(pv, fadd2(make_float2(__uint_as_float(rp[c]), __uint_as_float(rp[c + 1])), nd2));
-            dk[c >> 1] = pack_bf16x2(ds.x, ds.y);
+            for (int c = 0; c < 32; c += 2) {
+              const float2 y = ffma2(make_float2(__uint_as_float(rs[c]), __uint_as_float(rs[c + 1])), sl2, nl2);
+              const float2 pv = make_float2(ex2_approx(y.x), ex2_approx(y.y));  // -inf -> 0
+              const float2 ds = fmul2(pv, fadd2(make_float2(__uint_as_float(rp[c]), __uint_as_float(rp[c + 1])), nd2));
+              res2 = fadd2(res2, ds);
+              dk[c >> 1] = pack_bf16x2(ds.x, ds.y);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const float2 y = ffma2(make_float2(__uint_as_float(rs[c]), __uint_as_float(rs[c + 1])), sl2, nl2);
+              dk[c >> 1] = pack_bf16x2(-res * ex2_approx(y.x), -res * ex2_approx(y.y));
+            }
           }
           tmem_st16(trow + cS + cbase + half * 16, dk);
         }
+        if (it + 1 == kr.n1) sRes[(item & 1) * 256 + wg * 128 + row] = res2.x + res2.y;
         tmem_st_wait();
         tc_fence_before();
+        if (it + 1 == kr.n1) mbar_arrive_warp(&bars->r_full);
         mbar_arrive_warp(&bars->ds_full);
       }
+      if (ok && kr.nt == kr.n1) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->r_full, item & 1, w, kSiteRes));
+        const float* s = sRes + (item & 1) * 256 + row;
+        res = s[0] + s[128];
+      }
+      if (ok && store && wg == 0) a.delta[tab] = nd - res;  // -(Delta + r): both warpgroups have read it
       // ------------------------------------------------------------ epilogue: dQ rows
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->dq_done[(n - 1) & 1], ((n - 1) >> 1) & 1, w, kSiteEpi));
       if (ok) {

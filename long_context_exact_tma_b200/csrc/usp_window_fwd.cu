@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_expect_tx_w(&full[s], C::kTileBytes);
         for (int p = 0; p < C::kPanels; ++p)
           tma_load_4d_w(tm, &full[s], sbuf + s * C::kTileBytes + p * C::kPanelBytes, p * 64, x.h / g.G,
-                        kr.tile(it) * kBN, x.b);
+                        kr.base(it), x.b);
         ++issued;
         if (kside && it == 0) {
           // Q behind the first K: its buffer frees last, when the previous item's last S is done
@@ -202,42 +202,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ UMMA issuer
-    constexpr uint32_t kIdescQK = idesc_bf16_f32(kBM, kBN, 0, 0);
     constexpr uint32_t kIdescPV = idesc_bf16_f32(kBM, D, 0, 1);
     const uint64_t dQ0 = sdesc_sw128(smem_addr(sQ), 16, 1024);
     const uint64_t dK0 = sdesc_sw128(smem_addr(sK), 16, 1024);
     const uint64_t dV0 = sdesc_sw128(smem_addr(sV), C::kPanelBytes, 1024);
-    auto issue_s = [&](int t, int ks) {  // S_t = Q_t K^T, K from stage ks
+    auto issue_s = [&](int t, int ks, int keys) {  // S_t = Q_t K^T, the first `keys` keys of stage ks
+      const uint32_t idesc = idesc_bf16_f32(kBM, keys, 0, 0);
       const uint64_t qd = dQ0 + ((t * C::kTileBytes) >> 4), kd = dK0 + ((ks * C::kTileBytes) >> 4);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = ((kk >> 2) * C::kPanelBytes + (kk & 3) * 32) >> 4;
-        umma_bf16_w(tmem + col_s(t), qd + off, kd + off, kIdescQK, kk > 0 ? 1u : 0u);
+        umma_bf16_w(tmem + col_s(t), qd + off, kd + off, idesc, kk > 0 ? 1u : 0u);
       }
       umma_commit_w(&bars->s_full[t]);
     };
-    auto tiles_of = [&](int idx) {
+    auto run_of = [&](int idx) {
       const Item x = item_of(g, idx);
-      return key_run(g, x.q0, x.q_end(g)).nt;
+      return key_run(g, x.q0, x.q_end(g));
     };
     bool ok = true, issued_any = false;
     int idx = blockIdx.x;
     if (idx < a.n_items) {
-      int nt = tiles_of(idx), it = 0, item = 0;
+      KeyRun kr = run_of(idx);
+      int it = 0, item = 0;
       ok = mbar_wait_w(&bars->q_full, 0, w, kSiteQ) && mbar_wait_w(&bars->k_full[0], 0, w, kSiteK);
       if (ok) {
         tc_fence_after();
-        issue_s(0, 0);
-        issue_s(1, 0);
+        issue_s(0, 0, kr.width(0));
+        issue_s(1, 0, kr.width(0));
         umma_commit_w(&bars->k_empty[0]);
-        if (nt == 1) umma_commit_w(&bars->q_empty);
+        if (kr.nt == 1) umma_commit_w(&bars->q_empty);
         issued_any = true;
       }
       for (int n = 0; ok; ++n) {  // n: key tile of the CTA's stream, it: of the item
         const int s = n % C::kVSt, s1 = (n + 1) % C::kKSt;
-        const bool last = it + 1 == nt;
+        const bool last = it + 1 == kr.nt;
         const bool more = !last || idx + stride < a.n_items;
-        const int next_nt = last && more ? tiles_of(idx + stride) : nt;
+        const KeyRun next_kr = last && more ? run_of(idx + stride) : kr;
+        const int next_it = last ? 0 : it + 1;
+        const int pv_steps = kr.width(it) / 16;  // 16-key steps of this tile's products: 1, 2 or 8
         if (!mbar_wait_w(&bars->v_full[s], (n / C::kVSt) & 1, w, kSiteV)) { ok = false; break; }
         const uint64_t vd = dV0 + ((s * C::kTileBytes) >> 4);
         auto issue_pv = [&](int t) -> bool {  // in two halves of 64 keys, each as soon as its P is in TMEM
@@ -245,13 +248,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kBN / 32; ++kk)
-            umma_bf16_tmem_a_w(tmem + col_o(t), tmem + col_s(t) + kk * 8, vd + ((kk * 16 * 128) >> 4), kIdescPV,
-                               (it > 0 || kk > 0) ? 1u : 0u);
+            if (kk < pv_steps)
+              umma_bf16_tmem_a_w(tmem + col_o(t), tmem + col_s(t) + kk * 8, vd + ((kk * 16 * 128) >> 4), kIdescPV,
+                                 (it > 0 || kk > 0) ? 1u : 0u);
           if (!mbar_wait_w(&bars->p_full[t], n & 1, w, kSiteP)) return false;
           tc_fence_after();
+          if (pv_steps == kBN / 16) {
 #pragma unroll
-          for (int kk = kBN / 32; kk < kBN / 16; ++kk)
-            umma_bf16_tmem_a_w(tmem + col_o(t), tmem + col_s(t) + kk * 8, vd + ((kk * 16 * 128) >> 4), kIdescPV, 1u);
+            for (int kk = kBN / 32; kk < kBN / 16; ++kk)
+              umma_bf16_tmem_a_w(tmem + col_o(t), tmem + col_s(t) + kk * 8, vd + ((kk * 16 * 128) >> 4), kIdescPV, 1u);
+          }
           umma_commit_w(&bars->pv_done[t]);
           if (t == 1) umma_commit_w(&bars->v_empty[s]);
           return true;
@@ -259,10 +265,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto next_s = [&](int t) -> bool {  // S_t of the next tile overwrites P_t: behind this tile's PV_t
           if (!mbar_wait_w(&bars->pv_done[t], n & 1, w, kSitePvDone)) return false;
           tc_fence_after();
-          issue_s(t, s1);
+          issue_s(t, s1, next_kr.width(next_it));
           if (t == 1) {
             umma_commit_w(&bars->k_empty[s1]);
-            if (last ? next_nt == 1 : it + 2 == nt) umma_commit_w(&bars->q_empty);
+            if (next_it + 1 == next_kr.nt) umma_commit_w(&bars->q_empty);
           }
           return true;
         };
@@ -276,12 +282,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok || !more) break;
         if (last) {
           idx += stride;
-          nt = next_nt;
-          it = 0;
           ++item;
-        } else {
-          ++it;
         }
+        kr = next_kr;
+        it = next_it;
       }
     }
     if (!ok && issued_any) {
@@ -304,15 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int h = x.h + t * x.dh, q0 = x.q0 + t * x.dq;
       const int i = q0 + row;
       const bool store = i < g.S;
-      // visible keys of the row: [lo, sink_end) and [first, i]; a row past the end sees nothing
-      int lo = 0, first = 0, sink_end = 0;
-      if (store) {
-        lo = win_lo(g, i);
-        first = max(lo, i - g.W + 1);
-        sink_end = min(lo + g.ns, i + 1);
-      } else {
-        first = INT_MAX;
-      }
+      const RowSpan span = row_span(g, i);
       // the first key that every row of the tile sees, and the row up to which every row sees
       const int q_last = min(q0 + kBM, g.S) - 1;
       const int first_all = q_last < q0 ? INT_MAX : max(win_lo(g, q_last), q_last - g.W + 1);
@@ -323,7 +319,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[t], n & 1, w, kSiteS));
         if (!ok) break;
         tc_fence_after();
-        const int k0 = kr.tile(it) * kBN;
+        const int k0 = kr.base(it);
+        const float2 sl2 = make_float2(g.scale_log2, g.scale_log2);
+        if (kr.sink(it) && kr.cols <= 32) {
+          // a narrow sink tile, always an item's first: one group of 32 columns, no O to rescale yet
+          uint32_t r[32];
+          tmem_ld32(trow + cS, r);
+          tmem_ld_wait();
+          reg_fence32(r);
+          const uint32_t vis = visible_bits(span, kr, it, k0, 0);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            if (!((vis >> c) & 1u)) r[c] = 0xFF800000u;
+            mx = fmaxf(mx, __uint_as_float(r[c]));
+          }
+          m_use = mx * g.scale_log2;
+          const float m_safe = m_use == -INFINITY ? 0.f : m_use;
+          float2 acc = make_float2(0.f, 0.f), accb = acc;
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float2 y = ffma2(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sl2,
+                                   make_float2(-m_safe, -m_safe));
+            const float2 pv = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            acc = fadd2(acc, pv);
+            pk[c >> 1] = pack_bf16x2(pv.x, pv.y);
+            accb = add_bf16x2_f32(accb, pk[c >> 1]);
+          }
+          l_run = acc.x + acc.y;
+          lb_run = accb.x + accb.y;
+          tmem_st16(trow + cS, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive_warp(&bars->p_half[t]);
+          mbar_arrive_warp(&bars->p_full[t]);
+          continue;
+        }
         uint32_t r0[32], r1[32], r2[32], r3[32];
         tmem_ld32(trow + cS + 0, r0);
         tmem_ld32(trow + cS + 32, r1);
@@ -336,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         reg_fence32(r3);
         if (!(k0 >= first_all && k0 + kBN - 1 <= q0)) {  // not visible as a whole: -inf where it is not
           auto hide = [&](uint32_t (&r)[32], int c0) {
-            const uint32_t vis = bits_between(first - k0, i + 1 - k0, c0) | bits_between(lo - k0, sink_end - k0, c0);
+            const uint32_t vis = visible_bits(span, kr, it, k0, c0);
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (!((vis >> c) & 1u)) r[c] = 0xFF800000u;
@@ -371,7 +403,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         float2 acc[4], accb[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[q] = accb[q] = make_float2(0.f, 0.f);
-        const float2 sl2 = make_float2(g.scale_log2, g.scale_log2);
         const float2 nm = make_float2(-m_safe, -m_safe);
         auto emit = [&](const uint32_t (&r)[32], uint32_t col) {
           uint32_t pk[16];

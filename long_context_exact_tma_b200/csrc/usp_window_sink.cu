@@ -1,17 +1,19 @@
 // usp_window_sink.cu -- backward of sliding-window attention with sinks: dK and
 // dV of the sinks from the far queries, those whose tile lies behind the band of
 // the sink's key tile (usp_window.cuh) and that the key-major kernel so never
-// visits. A query tile m has far sinks of one document only, that of its first
-// row: any other document with rows in m starts inside m.
+// visits. A query tile has far sinks of one document only, that of its first row:
+// any other document with rows in the tile starts inside it.
 //
 //   dV_s = sum_i P_is dO_i,  dK_s / scale = sum_i P_is (dO_i.v_s - Delta_i) Q_i
 //
 // A few keys against every query is bound by reading Q and dO once, so the
-// products run on the warp-level 16x8x16 matrix instruction (a 128-key tensor
-// tile would be 4 keys in 128): warp = 16 query rows, 16 sinks at a time. One CTA
-// per (query tile, kv head, batch) writes the fp32 sums over its rows and the
-// group's heads, warp by warp in a fixed order; a second kernel adds the tiles in
-// a fixed order. No atomics: the result does not depend on scheduling.
+// products run on the warp-level 16x8x16 matrix instruction (a 128-key tensor tile
+// would hold 4 keys in 128): warp = 16 query rows, 16 sinks at a time. A CTA takes
+// a run of query tiles of one document and kv head and streams its rows, tile by
+// tile and head by head; every warp fetches its own rows through its own ring of
+// cp.async buffers, so the loop has no block barrier. The warps' fp32 sums are
+// joined in a fixed order, and a second kernel adds the runs in a fixed order: no
+// atomics, the result does not depend on scheduling.
 #include <math.h>
 
 #include "usp_mma.cuh"
@@ -21,31 +23,34 @@
 namespace usp {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = 16;  // sinks at a time
+constexpr int kStages = 3;  // (tile, head) steps in flight
 
 struct FarArgs {
   WinGeo g;
   const __nv_bfloat16 *q, *k, *v, *dO;
   const float *lse2, *delta;
   int Lp;
-  float* part;
+  int chunk;    // tiles of a CTA: its runs start at multiples of it and where a document's tiles start
+  int n_chunks;
+  float* part;  // [b][kv head][first tile of the run][sink][2][D]
   float* sum;
 };
-
-// The sink at position j is far from query tile m.
-__device__ __forceinline__ bool is_far(const WinGeo& g, int j, int m) { return last_qtile(g, j / kBN) < m; }
 
 template <int D>
 struct FarCfg {
   static constexpr int kRowBytes = D * 2;
   static constexpr int kChunks = D / 8;  // 16-byte chunks of a row
-  static constexpr int kTile = kBM * kRowBytes;
-  static constexpr int kOffDO = kTile;
-  static constexpr int kOffK = 2 * kTile;
+  static constexpr int kHalf = 16 * kRowBytes;
+  static constexpr int kStageBytes = 2 * kHalf;  // a warp's 16 rows of Q, then of dO
+  static constexpr int kWarpBytes = kStages * kStageBytes;
+  static constexpr int kOffK = kWarps * kWarpBytes;
   static constexpr int kOffV = kOffK + kGroup * kRowBytes;
   static constexpr int kOffSum = kOffV + kGroup * kRowBytes;  // fp32 [kGroup][2][D]
   static constexpr int kSmemBytes = kOffSum + kGroup * 2 * D * 4;
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
 template <int D>
@@ -58,134 +63,157 @@ __global__ void __launch_bounds__(kThreads, 1) far_kernel(const FarArgs a) {
   using C = FarCfg<D>;
   extern __shared__ __align__(128) uint8_t smem[];
   const WinGeo& g = a.g;
-  const int m = blockIdx.x % g.n_tiles, gl = blockIdx.x / g.n_tiles % g.Hkv, b = blockIdx.x / g.n_tiles / g.Hkv;
+  const int cx = blockIdx.x % a.n_chunks, gl = blockIdx.x / a.n_chunks % g.Hkv, b = blockIdx.x / a.n_chunks / g.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int q0 = m * kBM;
-  int lo, hi;
-  win_span(g, q0, lo, hi);
-  const int n_sinks = min(g.ns, hi - lo);
-  if (!is_far(g, lo, m)) return;  // band ends grow with the key: no sink is far
-  const uint32_t s_base = smem_addr(smem);
+  const uint32_t base = smem_addr(smem), mine = base + warp * C::kWarpBytes;
   float* sums = reinterpret_cast<float*>(smem + C::kOffSum);
-  float* part = a.part + ((static_cast<size_t>(b) * g.Hkv + gl) * g.n_tiles + m) * g.ns * (2 * D);
+  const int m_end = min((cx + 1) * a.chunk, g.n_tiles);
 
-  for (int s0 = 0; s0 < n_sinks; s0 += kGroup) {
-    __syncthreads();
-    for (int x = tid; x < kGroup * C::kChunks; x += kThreads) {
-      const int r = x / C::kChunks, ch = x % C::kChunks;
-      uint4 kv = make_uint4(0, 0, 0, 0), vv = kv;
-      if (s0 + r < n_sinks) {
-        const size_t e = ((static_cast<size_t>(b) * g.S + lo + s0 + r) * g.Hkv + gl) * D + ch * 8;
-        kv = *reinterpret_cast<const uint4*>(a.k + e);
-        vv = *reinterpret_cast<const uint4*>(a.v + e);
-      }
-      *reinterpret_cast<uint4*>(smem + C::kOffK + at<D>(r, ch)) = kv;
-      *reinterpret_cast<uint4*>(smem + C::kOffV + at<D>(r, ch)) = vv;
-    }
-    for (int x = tid; x < kGroup * 2 * D; x += kThreads) sums[x] = 0.f;
-    // which of this lane's sink columns (2c, 2c+1 and 2c+8, 2c+9 of the group) are far
-    bool far[2][2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int s = s0 + u * 8 + (lane & 3) * 2 + e;
-        far[u][e] = s < n_sinks && is_far(g, lo + s, m);
-      }
-    float av[D / 8][4], ak[D / 8][4];
-#pragma unroll
-    for (int x = 0; x < D / 8; ++x)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) av[x][e] = ak[x][e] = 0.f;
+  for (int m0 = cx * a.chunk, m1; m0 < m_end; m0 = m1) {
+    // the run [m0, m1): tiles whose first rows are of one document [lo, hi)
+    int lo, hi;
+    win_span(g, m0 * kBM, lo, hi);
+    m1 = min(m_end, (hi - 1) / kBM + 1);
+    const int n_sinks = min(g.ns, hi - lo);
+    // band ends grow with the key: tiles from here on have far sinks
+    const int mf = max(m0, last_qtile(g, lo / kBN) + 1);
+    if (mf >= m1) continue;
+    float* part = a.part + ((static_cast<size_t>(b) * g.Hkv + gl) * g.n_tiles + m0) * g.ns * (2 * D);
+    const int steps = (m1 - mf) * g.G;
 
-    for (int hh = 0; hh < g.G; ++hh) {
-      const int h = gl * g.G + hh;
-      __syncthreads();  // the previous head's tiles have been read
-#pragma unroll 4
-      for (int x = tid; x < kBM * C::kChunks; x += kThreads) {
+    for (int s0 = 0; s0 < n_sinks; s0 += kGroup) {
+      auto fetch = [&](int st) {
+        if (st < steps) {
+          const int h = gl * g.G + st % g.G, row0 = (mf + st / g.G) * kBM + warp * 16;
+          const uint32_t dst = mine + (st % kStages) * C::kStageBytes;
+#pragma unroll
+          for (int y = 0; y < 16 * C::kChunks / 32; ++y) {
+            const int r = y * (32 / C::kChunks) + lane / C::kChunks, ch = lane % C::kChunks;
+            const bool ok = row0 + r < g.S;
+            const size_t e = ((static_cast<size_t>(b) * g.S + (ok ? row0 + r : 0)) * g.Hq + h) * D + ch * 8;
+            cp_async16(dst + at<D>(r, ch), a.q + e, ok);
+            cp_async16(dst + C::kHalf + at<D>(r, ch), a.dO + e, ok);
+          }
+        }
+        cp_async_commit();
+      };
+      for (int st = 0; st < kStages - 1; ++st) fetch(st);
+      __syncthreads();  // the previous group's sums have been written out
+      for (int x = tid; x < kGroup * C::kChunks; x += kThreads) {
         const int r = x / C::kChunks, ch = x % C::kChunks;
-        uint4 qv = make_uint4(0, 0, 0, 0), dv = qv;
-        if (q0 + r < g.S) {
-          const size_t e = ((static_cast<size_t>(b) * g.S + q0 + r) * g.Hq + h) * D + ch * 8;
-          qv = *reinterpret_cast<const uint4*>(a.q + e);
-          dv = *reinterpret_cast<const uint4*>(a.dO + e);
+        uint4 kv = make_uint4(0, 0, 0, 0), vv = kv;
+        if (s0 + r < n_sinks) {
+          const size_t e = ((static_cast<size_t>(b) * g.S + lo + s0 + r) * g.Hkv + gl) * D + ch * 8;
+          kv = *reinterpret_cast<const uint4*>(a.k + e);
+          vv = *reinterpret_cast<const uint4*>(a.v + e);
         }
-        *reinterpret_cast<uint4*>(smem + at<D>(r, ch)) = qv;
-        *reinterpret_cast<uint4*>(smem + C::kOffDO + at<D>(r, ch)) = dv;
+        *reinterpret_cast<uint4*>(smem + C::kOffK + at<D>(r, ch)) = kv;
+        *reinterpret_cast<uint4*>(smem + C::kOffV + at<D>(r, ch)) = vv;
+      }
+      for (int x = tid; x < kGroup * 2 * D; x += kThreads) sums[x] = 0.f;
+      __syncthreads();
+      // first far tile of this lane's sink columns (2c, 2c+1 and 2c+8, 2c+9 of the group)
+      int far_from[2][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int s = s0 + u * 8 + (lane & 3) * 2 + e;
+          far_from[u][e] = s < n_sinks ? last_qtile(g, (lo + s) / kBN) + 1 : INT_MAX;
+        }
+      float av[D / 8][4], ak[D / 8][4];
+#pragma unroll
+      for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) av[x][e] = ak[x][e] = 0.f;
+
+      for (int st = 0; st < steps; ++st) {
+        fetch(st + kStages - 1);
+        const int h = gl * g.G + st % g.G, m = mf + st / g.G;
+        const int i0 = m * kBM + warp * 16 + (lane >> 2);
+        const size_t tab = (static_cast<size_t>(b) * g.Hq + h) * a.Lp + i0;
+        float nl[2], nd[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          nl[half] = a.lse2[tab + half * 8];
+          nd[half] = a.delta[tab + half * 8];
+        }
+        cp_async_wait<kStages - 1>();
+        __syncwarp();
+        const uint32_t sq = mine + (st % kStages) * C::kStageBytes, sd = sq + C::kHalf;
+        // S = Q K^T, dP = dO V^T of 16 rows and 16 sinks
+        float sc[2][4] = {}, dp[2][4] = {};
+        const int ar = lane & 15, ac = lane >> 4;                              // A rows and half chunks
+        const int br = (lane & 7) + ((lane >> 4) << 3), bc = (lane >> 3) & 1;  // B: sinks and halves
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          uint32_t qa[4], da[4], kb[4], vb[4];
+          ldsm_x4(qa, sq + at<D>(ar, 2 * kk + ac));
+          ldsm_x4(da, sd + at<D>(ar, 2 * kk + ac));
+          ldsm_x4(kb, base + C::kOffK + at<D>(br, 2 * kk + bc));
+          ldsm_x4(vb, base + C::kOffV + at<D>(br, 2 * kk + bc));
+          mma_16816(sc[0], qa, kb[0], kb[1]);
+          mma_16816(sc[1], qa, kb[2], kb[3]);
+          mma_16816(dp[0], da, vb[0], vb[1]);
+          mma_16816(dp[1], da, vb[2], vb[3]);
+        }
+        uint32_t pt[4], dt[4];  // P^T, dS^T: sinks x rows
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {   // rows i0, i0 + 8
+          const bool live = i0 + half * 8 < hi;  // a row of the same document (hi <= S)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float p[2], ds[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              p[e] = live && m >= far_from[u][e] ? ex2_approx(sc[u][half * 2 + e] * g.scale_log2 + nl[half]) : 0.f;
+              ds[e] = p[e] * (dp[u][half * 2 + e] + nd[half]);
+            }
+            // bf16 operands, as P and dS have in the key-major kernel; sums stay fp32
+            pt[half * 2 + u] = mov_trans(pack_bf16x2(p[0], p[1]));
+            dt[half * 2 + u] = mov_trans(pack_bf16x2(ds[0], ds[1]));
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          uint32_t db[4], qb[4];
+          ldsm_x4_trans(db, sd + at<D>(ar, 2 * x + ac));
+          ldsm_x4_trans(qb, sq + at<D>(ar, 2 * x + ac));
+          mma_16816(av[2 * x], pt, db[0], db[1]);
+          mma_16816(av[2 * x + 1], pt, db[2], db[3]);
+          mma_16816(ak[2 * x], dt, qb[0], qb[1]);
+          mma_16816(ak[2 * x + 1], dt, qb[2], qb[3]);
+        }
+        __syncwarp();  // every lane has read the stage before it is filled again
+      }
+      for (int y = 0; y < kWarps; ++y) {  // warp by warp: a fixed order of the sum
+        __syncthreads();
+        if (warp == y) {
+#pragma unroll
+          for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const int s = (lane >> 2) + (e >> 1) * 8, d = x * 8 + (lane & 3) * 2;
+              float2* tk = reinterpret_cast<float2*>(sums + (s * 2 + 0) * D + d);
+              float2* tv = reinterpret_cast<float2*>(sums + (s * 2 + 1) * D + d);
+              *tk = make_float2(tk->x + ak[x][e], tk->y + ak[x][e + 1]);
+              *tv = make_float2(tv->x + av[x][e], tv->y + av[x][e + 1]);
+            }
+        }
       }
       __syncthreads();
-      // S = Q K^T, dP = dO V^T of 16 rows and 16 sinks
-      float sc[2][4] = {}, dp[2][4] = {};
-      const int ar = warp * 16 + (lane & 15), ac = lane >> 4;         // A rows and half chunks
-      const int br = (lane & 7) + ((lane >> 4) << 3), bc = (lane >> 3) & 1;  // B: sinks and halves
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        uint32_t qa[4], da[4], kb[4], vb[4];
-        ldsm_x4(qa, s_base + at<D>(ar, 2 * kk + ac));
-        ldsm_x4(da, s_base + C::kOffDO + at<D>(ar, 2 * kk + ac));
-        ldsm_x4(kb, s_base + C::kOffK + at<D>(br, 2 * kk + bc));
-        ldsm_x4(vb, s_base + C::kOffV + at<D>(br, 2 * kk + bc));
-        mma_16816(sc[0], qa, kb[0], kb[1]);
-        mma_16816(sc[1], qa, kb[2], kb[3]);
-        mma_16816(dp[0], da, vb[0], vb[1]);
-        mma_16816(dp[1], da, vb[2], vb[3]);
-      }
-      uint32_t pt[4], dt[4];  // P^T, dS^T: sinks x rows
-      const int i0 = q0 + warp * 16 + (lane >> 2);
-      const size_t tab = (static_cast<size_t>(b) * g.Hq + h) * a.Lp + i0;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {  // rows i0, i0 + 8
-        const bool live = i0 + half * 8 < hi;   // a row of the same document (hi <= S)
-        const float nl = a.lse2[tab + half * 8], nd = a.delta[tab + half * 8];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          float p[2], ds[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            p[e] = live && far[u][e] ? ex2_approx(sc[u][half * 2 + e] * g.scale_log2 + nl) : 0.f;
-            ds[e] = p[e] * (dp[u][half * 2 + e] + nd);
-          }
-          // bf16 operands, as P and dS have in the key-major kernel; sums stay fp32
-          pt[half * 2 + u] = mov_trans(pack_bf16x2(p[0], p[1]));
-          dt[half * 2 + u] = mov_trans(pack_bf16x2(ds[0], ds[1]));
-        }
-      }
-      const int tr = warp * 16 + (lane & 15), tc = lane >> 4;
-#pragma unroll
-      for (int x = 0; x < D / 16; ++x) {
-        uint32_t db[4], qb[4];
-        ldsm_x4_trans(db, s_base + C::kOffDO + at<D>(tr, 2 * x + tc));
-        ldsm_x4_trans(qb, s_base + at<D>(tr, 2 * x + tc));
-        mma_16816(av[2 * x], pt, db[0], db[1]);
-        mma_16816(av[2 * x + 1], pt, db[2], db[3]);
-        mma_16816(ak[2 * x], dt, qb[0], qb[1]);
-        mma_16816(ak[2 * x + 1], dt, qb[2], qb[3]);
-      }
+      const int n = min(kGroup, n_sinks - s0) * 2 * D;
+      for (int x = tid; x < n; x += kThreads) part[static_cast<size_t>(s0) * 2 * D + x] = sums[x];
     }
-    for (int y = 0; y < kThreads / 32; ++y) {  // warp by warp: a fixed order of the sum
-      __syncthreads();
-      if (warp == y) {
-#pragma unroll
-        for (int x = 0; x < D / 8; ++x)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int s = (lane >> 2) + (e >> 1) * 8, d = x * 8 + (lane & 3) * 2 + (e & 1);
-            sums[(s * 2 + 0) * D + d] += ak[x][e];
-            sums[(s * 2 + 1) * D + d] += av[x][e];
-          }
-      }
-    }
-    __syncthreads();
-    const int n = min(kGroup, n_sinks - s0) * 2 * D;
-    for (int x = tid; x < n; x += kThreads) part[static_cast<size_t>(s0) * 2 * D + x] = sums[x];
   }
+  cp_async_wait<0>();
 }
 
-// sum[b][gl][d][s] = the far tiles' partials of sink s of document d, in four
-// interleaved runs added in order.
+// sum[b][gl][d][s] = the partials of sink s of document d over the runs with far
+// tiles, in four interleaved series added in order.
 template <int D>
 __global__ void __launch_bounds__(8 * D) far_sum_kernel(const FarArgs a) {
-  __shared__ float run[4][2 * D];
+  __shared__ float series[4][2 * D];
   const WinGeo& g = a.g;
   const int s = blockIdx.x % g.ns, d = blockIdx.x / g.ns % g.n_docs;
   const int gl = blockIdx.x / g.ns / g.n_docs % g.Hkv, b = blockIdx.x / g.ns / g.n_docs / g.Hkv;
@@ -195,18 +223,22 @@ __global__ void __launch_bounds__(8 * D) far_sum_kernel(const FarArgs a) {
     hi = min(max(__ldg(g.cu + d + 1), lo), g.S);
   }
   if (lo + s >= hi) return;  // no such key: nothing reads its sum
-  const int m0 = last_qtile(g, (lo + s) / kBN) + 1, m1 = (hi - 1) / kBM;
+  // far tiles of the sink: [mf, me); its document's tiles start at md
+  const int mf = last_qtile(g, (lo + s) / kBN) + 1, me = (hi - 1) / kBM + 1, md = (lo + kBM - 1) / kBM;
   const int col = threadIdx.x % (2 * D), y = threadIdx.x / (2 * D);
   const size_t tile = static_cast<size_t>(g.ns) * 2 * D;
   const float* p = a.part + (static_cast<size_t>(b) * g.Hkv + gl) * g.n_tiles * tile + static_cast<size_t>(s) * 2 * D + col;
   float t = 0.f;
+  if (mf < me) {
+    const int c0 = mf / a.chunk, c1 = (me - 1) / a.chunk;
 #pragma unroll 8
-  for (int m = m0 + y; m <= m1; m += 4) t += p[m * tile];
-  run[y][col] = t;
+    for (int c = c0 + y; c <= c1; c += 4) t += p[static_cast<size_t>(max(c * a.chunk, md)) * tile];
+  }
+  series[y][col] = t;
   __syncthreads();
   if (y == 0)
     a.sum[(((static_cast<size_t>(b) * g.Hkv + gl) * g.n_docs + d) * g.ns + s) * (2 * D) + col] =
-        (run[0][col] + run[1][col]) + (run[2][col] + run[3][col]);
+        (series[0][col] + series[1][col]) + (series[2][col] + series[3][col]);
 }
 
 template <int D>
@@ -225,8 +257,13 @@ cudaError_t launch_d(const WinLaunch& L, cudaStream_t stream) {
   a.Lp = L.Lp;
   a.part = L.far_part;
   a.sum = L.far_sum;
-  const long long heads = static_cast<long long>(L.g.Hkv) * L.g.B, n_far = heads * L.g.n_tiles;
-  const long long n_sum = heads * L.g.n_docs * L.g.ns;
+  const long long heads = static_cast<long long>(L.g.Hkv) * L.g.B;
+  // Longer runs keep the ring of loads full and make fewer partials; a CTA per SM three times
+  // over is worth more.
+  a.chunk = 8;
+  while (a.chunk > 1 && heads * ((L.g.n_tiles + a.chunk - 1) / a.chunk) < 3LL * sm_count()) a.chunk /= 2;
+  a.n_chunks = (L.g.n_tiles + a.chunk - 1) / a.chunk;
+  const long long n_far = heads * a.n_chunks, n_sum = heads * L.g.n_docs * L.g.ns;
   if (n_far > 0x7FFFFFFFLL || n_sum > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
   far_kernel<D><<<static_cast<unsigned>(n_far), kThreads, C::kSmemBytes, stream>>>(a);
   note_launch();

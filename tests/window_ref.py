@@ -50,8 +50,13 @@ def forward_bounds(q, k, v, vis):
     return out, lse, (U * (1 + U) + E) * (A + out.abs()) + U * out.abs() + 1e-30, lse_tol
 
 
+FEW = 48  # rows of fewer keys have their dQ corrected for the rounding of out in Delta
+
+
 def backward(q, k, v, out, lse, do, vis):
-    """The formula with the given out and lse, in 64 bits: (dq, dk, dv) and their bounds."""
+    """The gradients with the given lse in 64 bits, (dq, dk, dv), and their bounds. Delta is the exact
+    sum_j P dP: the kernel corrects dO . out by the residue of its row, for dK and dV always, for dQ where
+    a row has fewer than FEW keys; elsewhere dQ may be off by |Delta - dO . out| |sum_j P k_j|."""
     B, S, Hq, D = q.shape
     Hkv = k.shape[2]
     G = Hq // Hkv
@@ -59,11 +64,16 @@ def backward(q, k, v, out, lse, do, vis):
     s = torch.einsum("bihd,bjhd->bhij", q, kk) / math.sqrt(D)
     p = torch.exp(s - lse.transpose(1, 2).unsqueeze(-1)).masked_fill(~vis, 0.0)
     dp = torch.einsum("bihd,bjhd->bhij", do, vv)
-    delta = (do * out).sum(-1).transpose(1, 2).unsqueeze(-1)
+    delta = (p * dp).sum(-1, keepdim=True)
+    given = (do * out).sum(-1).transpose(1, 2).unsqueeze(-1)
+    off = (delta - given).abs()
     ds = p * (dp - delta)
-    # dP and Delta are fp32 sums of D products
+    # dP, Delta and the residue are fp32 sums of D products each
     mag = torch.einsum("bihd,bjhd->bhij", do.abs(), vv.abs()) + (do * out).abs().sum(-1).transpose(1, 2).unsqueeze(-1)
-    ds_tol = (U + E) * ds.abs() + p * mag * 2.0 ** -24 * D
+    eps = 2.0 ** -24 * D * p * (mag + (p * mag).sum(-1, keepdim=True))
+    ds_tol = (U + E) * ds.abs() + eps
+    # dQ takes dS of the given Delta, rounded, then the correction, rounded
+    dq_tol = (U + E) * (p * (dp - given).abs() + p * off) + eps
     sc = 1 / math.sqrt(D)
 
     def group(x):
@@ -72,7 +82,8 @@ def backward(q, k, v, out, lse, do, vis):
     dq = torch.einsum("bhij,bjhd->bihd", ds, kk) * sc
     dk = group(torch.einsum("bhij,bihd->bjhd", ds, q)) * sc
     dv = group(torch.einsum("bhij,bihd->bjhd", p, do))
-    tq = torch.einsum("bhij,bjhd->bihd", ds_tol, kk.abs()) * sc * (1 + U) + U * dq.abs()
+    left = torch.einsum("bhij,bjhd->bihd", off * p, kk).abs() * sc * (vis.sum(-1) >= FEW).view(1, S, 1, 1)
+    tq = (torch.einsum("bhij,bjhd->bihd", dq_tol, kk.abs()) * sc + left) * (1 + U) + U * dq.abs()
     tk = group(torch.einsum("bhij,bihd->bjhd", ds_tol, q.abs())) * sc * (1 + U) + U * dk.abs()
     tv = group(torch.einsum("bhij,bihd->bjhd", p, do.abs())) * (U + E) * (1 + U) + U * dv.abs()
     return (dq, dk, dv), (tq + 1e-30, tk + 1e-30, tv + 1e-30)
