@@ -13,7 +13,7 @@
 //
 // Bound by memory: each element is read and written once. A thread takes one
 // 16-byte chunk column (two in the halves form) of one token and walks some of its
-// heads, so that the sines are computed once per walk; the lanes of a warp cover
+// heads, four at a time, so that the sines are computed once per walk; the lanes of a warp cover
 // neighbouring chunks and heads. Views whose rows are not 16-byte aligned take the
 // same kernel with one-element chunks.
 #include <math.h>
@@ -36,11 +36,27 @@ struct Job {
   long long s_b, s_t, s_h, d_b, d_t, d_h;
 };
 
+// n / d by a multiplication (n < 2^31): with m = 2^31 / d rounded up to 32 + shift bits, the
+// product's upper part is the quotient.
+struct Div {
+  uint32_t d, mul, shift;
+};
+Div make_div(uint32_t d) {
+  uint32_t shift = 0;
+  while ((1ull << shift) < d) ++shift;
+  const uint64_t m = ((1ull << (31 + shift)) + d - 1) / d;
+  return Div{d, static_cast<uint32_t>(m), shift};
+}
+__device__ __forceinline__ uint32_t quot(const Div& v, uint32_t n) {
+  return static_cast<uint32_t>((static_cast<uint64_t>(n) * v.mul) >> (31 + v.shift));
+}
+
 struct RopeArgs {
   Job job[USP_MAX_ROPE_JOBS];
-  int n_jobs, S, D, R, groups, pos64, inverse;
-  long long units;      // (token, group, chunk)
-  long long axis_step;  // tokens per axis of the position table
+  int n_jobs, D, R, pos64, inverse;
+  Div chunks, groups, S;   // chunks of a row, threads that share a token's chunk, tokens of a sequence
+  uint32_t tokens, slice;  // all tokens; those of one blockIdx.y
+  long long axis_step;     // tokens per axis of the position table
   const void* pos;
   unsigned long long turn[kMaxFreq];  // inv_freq / 2 pi as a fraction of 2^64
   unsigned char axis[kMaxFreq];
@@ -89,30 +105,50 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     s_axis[x] = a.axis[x];
   }
   __syncthreads();
-  const int n_rot = a.R / 2 / kF, n_chunks = n_rot + (a.D - a.R) / kV;
-  const long long u = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-  if (u >= a.units) return;
-  const int chunk = static_cast<int>(u % n_chunks);
-  const long long r = u / n_chunks;
-  const int grp = static_cast<int>(r % a.groups);
-  const long long token = r / a.groups;
-  const long long b = token / a.S, t = token % a.S;
+  const uint32_t n_rot = a.R / 2 / kF;
+  const uint32_t u = blockIdx.x * kThreads + threadIdx.x;  // (token of the slice, group, chunk)
+  const uint32_t r = quot(a.chunks, u), chunk = u - r * a.chunks.d;
+  const uint32_t tok = quot(a.groups, r), grp_ = r - tok * a.groups.d;
+  const uint32_t token = blockIdx.y * a.slice + tok;
+  if (tok >= a.slice || token >= a.tokens) return;
+  const int grp = static_cast<int>(grp_);
+  const uint32_t bq = quot(a.S, token);
+  const long long b = bq, t = token - bq * a.S.d;
   int j = 0;
   while (j + 1 < a.n_jobs && grp >= a.job[j + 1].g0) ++j;
   const Job& job = a.job[j];
   const int h0 = grp - job.g0;
   const T* src = static_cast<const T*>(job.src) + b * job.s_b + t * job.s_t;
   T* dst = static_cast<T*>(job.dst) + b * job.d_b + t * job.d_t;
-  if (chunk >= n_rot) {  // not rotated
-    const int e = a.R + (chunk - n_rot) * kV;
-    if (src == dst && job.s_h == job.d_h) return;
-    for (int h = h0; h < job.H; h += job.groups)
-      store<T, kV>(dst + h * job.d_h + e, load<T, kV>(src + h * job.s_h + e));
-    return;
-  }
+  // a chunk past R is copied (in place: left alone)
+  const bool rot = chunk < n_rot;
+  if (!rot && src == dst && job.s_h == job.d_h) return;
+  const int e1 = rot ? static_cast<int>(chunk) * kW : a.R + static_cast<int>(chunk - n_rot) * kV;
+  const int e2 = e1 + a.R / 2;  // the halves form's partner
+  // the first heads' chunks are on their way while the sines are made
+  constexpr int kAhead = 4;
+  Chunk<T, kW> x1s[kAhead], x2s[kPaired ? 1 : kAhead];
+  auto fetch = [&](int h) {
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y) {
+      const int hy = h + y * job.groups;
+      if (hy >= job.H) break;
+      const T* p = src + hy * job.s_h + e1;
+      if constexpr (kW == kV)
+        x1s[y] = load<T, kW>(p);
+      else if (rot)
+        x1s[y] = load<T, kW>(p);
+      else  // one element past R
+        x1s[y].e[0] = p[0];
+      if constexpr (!kPaired)
+        if (rot) x2s[y] = load<T, kV>(src + hy * job.s_h + e2);
+    }
+  };
+  fetch(h0);
   float c[kF], s[kF];
 #pragma unroll
   for (int f = 0; f < kF; ++f) {
+    if (!rot) break;
     const int fr = chunk * kF + f;
     const long long at = s_axis[fr] * a.axis_step + token;
     const long long p = a.pos64 ? static_cast<const long long*>(a.pos)[at] : static_cast<const int*>(a.pos)[at];
@@ -125,28 +161,40 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     }
     if (a.inverse) s[f] = -s[f];
   }
-  const int e1 = kPaired ? chunk * kW : chunk * kV, e2 = e1 + a.R / 2;
-#pragma unroll 4
-  for (int h = h0; h < job.H; h += job.groups) {
-    if constexpr (kPaired) {
-      Chunk<T, kW> x = load<T, kW>(src + h * job.s_h + e1);
+  for (int h = h0; h < job.H; h += kAhead * job.groups) {
+    if (h != h0) fetch(h);
 #pragma unroll
-      for (int f = 0; f < kF; ++f) {
-        const float x1 = widen(x.e[2 * f]), x2 = widen(x.e[2 * f + 1]);
-        x.e[2 * f] = narrow<T>(x1 * c[f] - x2 * s[f]);
-        x.e[2 * f + 1] = narrow<T>(x2 * c[f] + x1 * s[f]);
+    for (int y = 0; y < kAhead; ++y) {
+      const int hy = h + y * job.groups;
+      if (hy >= job.H) break;
+      Chunk<T, kW>& v1 = x1s[y];
+      T* const to = dst + hy * job.d_h + e1;
+      if (!rot) {
+        if constexpr (kW == kV)
+          store<T, kW>(to, v1);
+        else
+          to[0] = v1.e[0];
+        continue;
       }
-      store<T, kW>(dst + h * job.d_h + e1, x);
-    } else {
-      Chunk<T, kV> y1 = load<T, kV>(src + h * job.s_h + e1), y2 = load<T, kV>(src + h * job.s_h + e2);
+      if constexpr (kPaired) {
 #pragma unroll
-      for (int f = 0; f < kF; ++f) {
-        const float x1 = widen(y1.e[f]), x2 = widen(y2.e[f]);
-        y1.e[f] = narrow<T>(x1 * c[f] - x2 * s[f]);
-        y2.e[f] = narrow<T>(x2 * c[f] + x1 * s[f]);
+        for (int f = 0; f < kF; ++f) {
+          const float x1 = widen(v1.e[2 * f]), x2 = widen(v1.e[2 * f + 1]);
+          v1.e[2 * f] = narrow<T>(x1 * c[f] - x2 * s[f]);
+          v1.e[2 * f + 1] = narrow<T>(x2 * c[f] + x1 * s[f]);
+        }
+        store<T, kW>(to, v1);
+      } else {
+        Chunk<T, kV>& v2 = x2s[y];
+#pragma unroll
+        for (int f = 0; f < kF; ++f) {
+          const float x1 = widen(v1.e[f]), x2 = widen(v2.e[f]);
+          v1.e[f] = narrow<T>(x1 * c[f] - x2 * s[f]);
+          v2.e[f] = narrow<T>(x2 * c[f] + x1 * s[f]);
+        }
+        store<T, kV>(to, v1);
+        store<T, kV>(to + a.R / 2, v2);
       }
-      store<T, kV>(dst + h * job.d_h + e1, y1);
-      store<T, kV>(dst + h * job.d_h + e2, y2);
     }
   }
 }
@@ -154,25 +202,32 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 template <class T, int kV, bool kPaired>
 cudaError_t launch(RopeArgs& a, long long tokens, cudaStream_t st) {
   constexpr int kF = kPaired ? (kV + 1) / 2 : kV;
-  const long long n_chunks = a.R / 2 / kF + (a.D - a.R) / kV;
+  const uint32_t n_chunks = a.R / 2 / kF + (a.D - a.R) / kV;
   // Heads per thread: as many as pay the sines back, fewer while the tokens alone do not fill the machine.
   int per = kHeadsPerThread;
   auto groups_at = [&](int hp) {
-    int n = 0;
+    uint32_t n = 0;
     for (int j = 0; j < a.n_jobs; ++j) n += (a.job[j].H + hp - 1) / hp;
     return n;
   };
   while (per > 1 && tokens * n_chunks * groups_at(per) < 148LL * 1024) per /= 2;
-  a.groups = 0;
+  int groups = 0;
   for (int j = 0; j < a.n_jobs; ++j) {
-    a.job[j].g0 = a.groups;
+    a.job[j].g0 = groups;
     a.job[j].groups = (a.job[j].H + per - 1) / per;
-    a.groups += a.job[j].groups;
+    groups += a.job[j].groups;
   }
-  a.units = tokens * n_chunks * a.groups;
-  const long long blocks = (a.units + kThreads - 1) / kThreads;
-  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  rope_kernel<T, kV, kPaired><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(a);
+  const long long lanes = static_cast<long long>(n_chunks) * groups;  // threads of a token
+  if (lanes >= 1LL << 30) return cudaErrorInvalidConfiguration;
+  a.chunks = make_div(n_chunks);
+  a.groups = make_div(groups);
+  a.tokens = static_cast<uint32_t>(tokens);
+  // thread numbers of a slice stay below 2^31
+  const long long most = ((1LL << 31) - kThreads) / lanes;
+  a.slice = static_cast<uint32_t>(tokens < most ? tokens : most);
+  const long long blocks = (a.slice * lanes + kThreads - 1) / kThreads, slices = (tokens + a.slice - 1) / a.slice;
+  if (slices > 65535) return cudaErrorInvalidConfiguration;
+  rope_kernel<T, kV, kPaired><<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(slices)), kThreads, 0, st>>>(a);
   note_launch();
   return cudaGetLastError();
 }
@@ -227,11 +282,13 @@ extern "C" int usp_rope_axes(const usp_rope_job* jobs, int n_jobs, int B, int S,
     a.job[x].d_b = j.d_b; a.job[x].d_t = j.d_t; a.job[x].d_h = j.d_h;
   }
   a.n_jobs = n_jobs;
-  a.S = S; a.D = D; a.R = R;
+  const long long tokens = static_cast<long long>(B) * S;
+  if (tokens >= 1LL << 31) return record_error(USP_ERR_UNSUPPORTED, "too many rows");
+  a.S = make_div(S);
+  a.D = D; a.R = R;
   a.pos = positions;
   a.pos64 = pos_bits == 64;
   a.inverse = inverse;
-  const long long tokens = static_cast<long long>(B) * S;
   a.axis_step = tokens;
   for (int f = 0; f < R / 2; ++f) {
     if (!isfinite(inv_freq[f])) return record_error(USP_ERR_INVALID_ARG, "inv_freq[%d] is not finite", f);

@@ -5,13 +5,15 @@
 //
 // Bound by reading the visible cache rows once: 4 D bytes per key and kv head
 // against 4 D flops per key and query row. The n tokens of the heads of a group
-// share the kv head's rows, up to 16 query rows per warp tile, so the products run
-// on the 16x8x16 warp-level matrix instruction, whose rate is far above what the
-// memory feeds. The keys are split over CTAs and inside a CTA over its warps: each
-// warp streams 16 keys at a time through its own ring of cp.async buffers (no
-// block barrier in the loop), keeps its own running maximum, sum and O, and the
-// warps' results are joined at the end. With more than one split the CTAs write
-// fp32 partials that the log-sum-exp merge joins.
+// share the kv head's rows, 16 query rows per warp tile, so the products run on the
+// 16x8x16 warp-level matrix instruction, whose rate is far above what the memory
+// feeds. The keys are split over CTAs and inside a CTA over four streams: a stream
+// is one warp that takes 16 keys at a time, or two that share 32 when there are more
+// than 16 query rows, from its own ring of cp.async buffers (no block
+// barrier in the loop) with its own running maximum, sum and O. The streams'
+// results are joined in shared memory; up to 8 splits form a cluster and join
+// through distributed shared memory in the same launch, more write fp32 partials
+// that a second kernel joins by their LSE.
 #include <math.h>
 
 #include "../../include/usp.h"
@@ -22,10 +24,8 @@
 namespace usp {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kUnit = 16;   // keys of a warp's step
-constexpr int kStages = 3;  // steps in flight per warp
+constexpr int kStreams = 4;
+constexpr int kMaxCluster = 8;  // splits that join in one launch (the portable cluster size)
 constexpr int kMaxSplits = 64;
 constexpr int kSms = 148;
 
@@ -33,35 +33,56 @@ struct DecArgs {
   const __nv_bfloat16 *q, *k, *v;
   const int* lens;
   long long k_sn, k_st, k_sh, v_sn, v_st, v_sh;
-  __nv_bfloat16* out;  // one split
+  __nv_bfloat16* out;
   float* lse;
-  float* o_part;       // more: [n_splits][N*n*Hq][D]
+  float* o_part;  // [n_splits][N*n*Hq][D] without a cluster
   float* lse_part;
-  int N, n, cap, Hq, Hkv, G, W, ns, n_splits, row_tiles;
+  int N, n, cap, Hq, Hkv, G, W, ns;
+  int n_splits, cluster;  // cluster: n_splits, or 1 (then more splits write partials)
+  int row_blocks;
   float scale_log2;
 };
 
-template <int D>
+// kRt: row tiles (warps) of a stream. One leaves room for two CTAs on an SM, two
+// take more steps in flight instead.
+template <int D, int kRt>
 struct DecCfg {
+  static constexpr int kThreads = 32 * kStreams * kRt;
+  static constexpr int kUnit = 16 * kRt;  // keys of a stream's step
+  static constexpr int kStages = 3;
   static constexpr int kChunks = D / 8;
   static constexpr int kRowBytes = D * 2;
   static constexpr int kStageBytes = 2 * kUnit * kRowBytes;  // K then V
-  static constexpr int kWarpBytes = kStages * kStageBytes;
-  static constexpr int kSmemBytes = kWarps * kWarpBytes;
-  // the warps' results: O [16][D] fp32 over the warp's own buffers, then m, l, lb per row
-  static_assert(16 * D * 4 + 3 * 16 * 4 <= kWarpBytes, "results fit over the buffers");
+  static constexpr int kStreamBytes = kStages * kStageBytes;
+  static constexpr int kSmemBytes = kStreams * kStreamBytes;
+  // a stream's results over its own buffers: O [16 kRt][D] fp32, then m, l, lb per row
+  static constexpr int kRows = 16 * kRt;
+  static_assert(kRows * D * 4 + 3 * kRows * 4 <= kStreamBytes, "results fit over the buffers");
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 2) window_decode_kernel(const DecArgs a) {
-  using C = DecCfg<D>;
+__device__ __forceinline__ float ld_peer(const float* p, int rank) {  // this address in the cluster's CTA `rank`
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+template <int D, int kRt>
+__global__ void __launch_bounds__(DecCfg<D, kRt>::kThreads, kRt == 1 ? 2 : 1) window_decode_kernel(const DecArgs a) {
+  using C = DecCfg<D, kRt>;
+  constexpr int kUnit = C::kUnit;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g4 = lane >> 2, c4 = lane & 3;
+  const int stream = warp & (kStreams - 1), wrt = warp / kStreams;  // the warp's stream and row tile
   int x = blockIdx.x;
-  const int split = x % a.n_splits;
+  const int split = x % a.n_splits;  // a cluster is the splits of one (sequence, kv head, rows)
   x /= a.n_splits;
-  const int rt = x % a.row_tiles;
-  x /= a.row_tiles;
+  const int rb = x % a.row_blocks;
+  x /= a.row_blocks;
   const int kvh = x % a.Hkv, seq = x / a.Hkv;
   const int rows = a.n * a.G;  // rows of a (sequence, kv head): token major, then head of the group
   const int len = min(max(__ldg(a.lens + seq), 0), a.cap);
@@ -73,18 +94,18 @@ __global__ void __launch_bounds__(kThreads, 2) window_decode_kernel(const DecArg
   const int per = ((total + a.n_splits - 1) / a.n_splits + kUnit - 1) / kUnit * kUnit;
   const int x0 = min(split * per, total), x1 = min(x0 + per, total);
   const int units = (x1 - x0 + kUnit - 1) / kUnit;
-  const int mine = units > warp ? (units - warp + kWarps - 1) / kWarps : 0;  // this warp's: warp, warp + kWarps, ...
+  const int mine = units > stream ? (units - stream + kStreams - 1) / kStreams : 0;  // stream, stream + kStreams, ...
 
-  const uint32_t buf = smem_addr(smem) + warp * C::kWarpBytes;
+  const uint32_t buf = smem_addr(smem) + stream * C::kStreamBytes;
   const __nv_bfloat16* kb = a.k + seq * a.k_sn + kvh * a.k_sh;
   const __nv_bfloat16* vb = a.v + seq * a.v_sn + kvh * a.v_sh;
-  auto fetch = [&](int it) {
+  auto fetch = [&](int it) {  // the stream's warps share the rows of a step
     if (it < mine) {
-      const int base = x0 + (warp + it * kWarps) * kUnit;
-      const uint32_t dst = buf + (it % kStages) * C::kStageBytes;
+      const int base = x0 + (stream + it * kStreams) * kUnit;
+      const uint32_t dst = buf + (it % C::kStages) * C::kStageBytes;
 #pragma unroll
-      for (int y = 0; y < kUnit * C::kChunks / 32; ++y) {
-        const int r = y * (32 / C::kChunks) + lane / C::kChunks, ch = lane % C::kChunks;
+      for (int y = 0; y < kUnit * C::kChunks / 32 / kRt; ++y) {
+        const int r = (y * kRt + wrt) * (32 / C::kChunks) + lane / C::kChunks, ch = lane % C::kChunks;
         const int xi = base + r;
         const bool ok = xi < x1;
         const long long key = ok ? (xi < sE ? xi : wlo + xi - sE) : 0;
@@ -95,14 +116,20 @@ __global__ void __launch_bounds__(kThreads, 2) window_decode_kernel(const DecArg
     }
     cp_async_commit();
   };
-  for (int it = 0; it < kStages - 1; ++it) fetch(it);
+  auto stream_sync = [&]() {
+    if constexpr (kRt == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + stream), "n"(32 * kRt) : "memory");
+  };
+  for (int it = 0; it < C::kStages - 1; ++it) fetch(it);
 
   // Q fragments of rows g4 and g4 + 8 of the row tile; the rows' positions
   uint32_t qf[D / 16][4];
   int pos[2];
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    const int r = rt * 16 + g4 + half * 8;
+    const int r = (rb * kRt + wrt) * 16 + g4 + half * 8;
     const bool live = r < rows;
     pos[half] = live ? len - a.n + r / a.G : -1;  // -1: sees nothing
     const __nv_bfloat16* p =
@@ -121,23 +148,27 @@ __global__ void __launch_bounds__(kThreads, 2) window_decode_kernel(const DecArg
   float m_use[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lb[2] = {0.f, 0.f};
 
   for (int it = 0; it < mine; ++it) {
-    fetch(it + kStages - 1);
-    cp_async_wait<kStages - 1>();
-    __syncwarp();
-    const uint32_t sk = buf + (it % kStages) * C::kStageBytes, sv = sk + kUnit * C::kRowBytes;
-    float sc[2][4] = {};
+    cp_async_wait<C::kStages - 2>();
+    stream_sync();  // the step's rows are there, and every warp is done with the stage that is filled next
+    fetch(it + C::kStages - 1);
+    const uint32_t sk = buf + (it % C::kStages) * C::kStageBytes, sv = sk + kUnit * C::kRowBytes;
+    constexpr int kN = kUnit / 8;  // 8-key column tiles
+    float sc[kN][4] = {};
     const int br = (lane & 7) + ((lane >> 4) << 3), bc = (lane >> 3) & 1;
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-      uint32_t kf[4];
-      ldsm_x4(kf, sk + br * C::kRowBytes + (((2 * kk + bc) ^ (br & 7)) << 4));
-      mma_16816(sc[0], qf[kk], kf[0], kf[1]);
-      mma_16816(sc[1], qf[kk], kf[2], kf[3]);
+#pragma unroll
+      for (int u = 0; u < kN; u += 2) {
+        uint32_t kf[4];
+        ldsm_x4(kf, sk + (br + u * 8) * C::kRowBytes + (((2 * kk + bc) ^ (br & 7)) << 4));
+        mma_16816(sc[u], qf[kk], kf[0], kf[1]);
+        mma_16816(sc[u + 1], qf[kk], kf[2], kf[3]);
+      }
     }
-    const int base = x0 + (warp + it * kWarps) * kUnit;
+    const int base = x0 + (stream + it * kStreams) * kUnit;
     float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < kN; ++u)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int xi = base + u * 8 + c4 * 2 + (e & 1), p = pos[e >> 1];
@@ -165,10 +196,10 @@ __global__ void __launch_bounds__(kThreads, 2) window_decode_kernel(const DecArg
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[y][e] *= alpha[e >> 1];
     }
-    uint32_t pa[4];
+    uint32_t pa[kN / 2][4];
     float rs[2] = {0.f, 0.f}, rb[2] = {0.f, 0.f};
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < kN; ++u)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const float ms = m_use[half] == -INFINITY ? 0.f : m_use[half];
@@ -177,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_decode_kernel(const DecArg
         rs[half] += p0 + p1;
         const float2 w = add_bf16x2_f32(make_float2(0.f, 0.f), pk);
         rb[half] += w.x + w.y;  // O is divided by the sum of the rounded weights that made it
-        pa[u * 2 + half] = pk;
+        pa[u / 2][(u & 1) * 2 + half] = pk;
       }
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -187,105 +218,243 @@ __global__ void __launch_bounds__(kThreads, 2) window_decode_kernel(const DecArg
     const int vr = lane & 15, vc = lane >> 4;
 #pragma unroll
     for (int y = 0; y < D / 16; ++y) {
-      uint32_t vf[4];
-      ldsm_x4_trans(vf, sv + vr * C::kRowBytes + (((2 * y + vc) ^ (vr & 7)) << 4));
-      mma_16816(o[2 * y], pa, vf[0], vf[1]);
-      mma_16816(o[2 * y + 1], pa, vf[2], vf[3]);
+#pragma unroll
+      for (int u = 0; u < kN / 2; ++u) {
+        uint32_t vf[4];
+        ldsm_x4_trans(vf, sv + (vr + u * 16) * C::kRowBytes + (((2 * y + vc) ^ (vr & 7)) << 4));
+        mma_16816(o[2 * y], pa[u], vf[0], vf[1]);
+        mma_16816(o[2 * y + 1], pa[u], vf[2], vf[3]);
+      }
     }
-    __syncwarp();  // every lane has read the stage before it is filled again
   }
   cp_async_wait<0>();
-  __syncwarp();
-  // the warp's result over its own buffers
-  float* wo = reinterpret_cast<float*>(smem + warp * C::kWarpBytes);
-  float* ws = wo + 16 * D;
+  __syncthreads();
+  // the warp's result over its stream's buffers
+  float* wo = reinterpret_cast<float*>(smem + stream * C::kStreamBytes);
+  float* ws = wo + C::kRows * D;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
     l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
     lb[half] += __shfl_xor_sync(0xffffffffu, lb[half], 1);
     lb[half] += __shfl_xor_sync(0xffffffffu, lb[half], 2);
-    const int r = g4 + half * 8;
+    const int r = wrt * 16 + g4 + half * 8;
     if (c4 == 0) {
       ws[r] = m_use[half];
-      ws[16 + r] = l[half];
-      ws[32 + r] = lb[half];
+      ws[C::kRows + r] = l[half];
+      ws[2 * C::kRows + r] = lb[half];
     }
 #pragma unroll
     for (int y = 0; y < D / 8; ++y)
       *reinterpret_cast<float2*>(wo + r * D + y * 8 + c4 * 2) = make_float2(o[y][2 * half], o[y][2 * half + 1]);
   }
   __syncthreads();
-  // join the warps: eight threads per row
-  const int r = threadIdx.x >> 3, sub = threadIdx.x & 7, gr = rt * 16 + r;
-  if (gr >= rows) return;
-  float m = -INFINITY;
+  // join the streams: eight threads per row, each with its columns sub * 4 + 32 y
+  const int r = threadIdx.x >> 3, sub = threadIdx.x & 7, gr = rb * C::kRows + r;
+  float m = -INFINITY, lt = 0.f, lbt = 0.f, f[kStreams];
+  float4 t[D / 32];
+  {
 #pragma unroll
-  for (int y = 0; y < kWarps; ++y) m = fmaxf(m, reinterpret_cast<float*>(smem + y * C::kWarpBytes)[16 * D + r]);
-  const float ms = m == -INFINITY ? 0.f : m;
-  float lt = 0.f, lbt = 0.f, f[kWarps];
+    for (int y = 0; y < kStreams; ++y)
+      m = fmaxf(m, reinterpret_cast<float*>(smem + y * C::kStreamBytes)[C::kRows * D + r]);
+    const float ms = m == -INFINITY ? 0.f : m;
 #pragma unroll
-  for (int y = 0; y < kWarps; ++y) {
-    const float* s = reinterpret_cast<float*>(smem + y * C::kWarpBytes) + 16 * D;
-    f[y] = ex2_approx(s[r] - ms);
-    lt += f[y] * s[16 + r];
-    lbt += f[y] * s[32 + r];
+    for (int y = 0; y < kStreams; ++y) {
+      const float* s = reinterpret_cast<float*>(smem + y * C::kStreamBytes) + C::kRows * D;
+      f[y] = ex2_approx(s[r] - ms);
+      lt += f[y] * s[C::kRows + r];
+      lbt += f[y] * s[2 * C::kRows + r];
+    }
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {
+      t[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int y = 0; y < kStreams; ++y) {
+        const float4 w = *reinterpret_cast<const float4*>(smem + y * C::kStreamBytes + (r * D + sub * 4 + e * 32) * 4);
+        t[e].x += f[y] * w.x;
+        t[e].y += f[y] * w.y;
+        t[e].z += f[y] * w.z;
+        t[e].w += f[y] * w.w;
+      }
+    }
   }
+  bool write = gr < rows;
+  if (a.cluster > 1) {
+    // the CTA's result in place of stream 0's (every element is read and written by one thread),
+    // then each CTA joins every cluster-th row
+    float* co = reinterpret_cast<float*>(smem);
+    float* cs = co + C::kRows * D;
+    __syncwarp();  // a row's threads have read the streams' m, l, lb
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) *reinterpret_cast<float4*>(co + r * D + sub * 4 + e * 32) = t[e];
+    if (sub == 0) {
+      cs[r] = m;
+      cs[C::kRows + r] = lt;
+      cs[2 * C::kRows + r] = lbt;
+    }
+    cluster_sync();
+    write = write && r % a.cluster == split;
+    if (write) {
+      m = -INFINITY;
+      for (int c = 0; c < a.cluster; ++c) m = fmaxf(m, ld_peer(cs + r, c));
+      const float ms = m == -INFINITY ? 0.f : m;
+      lt = lbt = 0.f;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) t[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c = 0; c < a.cluster; ++c) {
+        const float w = ex2_approx(ld_peer(cs + r, c) - ms);
+        lt += w * ld_peer(cs + C::kRows + r, c);
+        lbt += w * ld_peer(cs + 2 * C::kRows + r, c);
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) {
+          const float* p = co + r * D + sub * 4 + e * 32;
+          t[e].x += w * ld_peer(p, c);
+          t[e].y += w * ld_peer(p + 1, c);
+          t[e].z += w * ld_peer(p + 2, c);
+          t[e].w += w * ld_peer(p + 3, c);
+        }
+      }
+    }
+    cluster_sync();  // no CTA ends while another reads its results
+  }
+  if (!write) return;
   const float inv = lbt > 0.f ? 1.f / lbt : 0.f;
   const float lse = lt > 0.f ? (m + __log2f(lt)) * 0.6931471805599453f : -INFINITY;
   const long long orow =
       (static_cast<long long>(seq) * a.n + gr / a.G) * a.Hq + static_cast<long long>(kvh) * a.G + gr % a.G;
   const long long n_rows = static_cast<long long>(a.N) * a.n * a.Hq;
+  const bool last = a.n_splits == a.cluster;  // the joined result, not a partial
 #pragma unroll
-  for (int d = sub * 4; d < D; d += 32) {
-    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int y = 0; y < kWarps; ++y) {
-      const float4 w = *reinterpret_cast<const float4*>(smem + y * C::kWarpBytes + (r * D + d) * 4);
-      t.x += f[y] * w.x;
-      t.y += f[y] * w.y;
-      t.z += f[y] * w.z;
-      t.w += f[y] * w.w;
-    }
-    if (a.n_splits == 1) {
+  for (int e = 0; e < D / 32; ++e) {
+    const int d = sub * 4 + e * 32;
+    if (last) {
       uint2 pk;
-      pk.x = pack_bf16x2(t.x * inv, t.y * inv);
-      pk.y = pack_bf16x2(t.z * inv, t.w * inv);
+      pk.x = pack_bf16x2(t[e].x * inv, t[e].y * inv);
+      pk.y = pack_bf16x2(t[e].z * inv, t[e].w * inv);
       *reinterpret_cast<uint2*>(a.out + orow * D + d) = pk;
     } else {
       *reinterpret_cast<float4*>(a.o_part + (split * n_rows + orow) * D + d) =
-          make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv);
+          make_float4(t[e].x * inv, t[e].y * inv, t[e].z * inv, t[e].w * inv);
     }
   }
   if (sub == 0) {
-    if (a.n_splits == 1)
+    if (last)
       a.lse[orow] = lse;
     else
       a.lse_part[split * n_rows + orow] = lse;
   }
 }
 
+// The partials' join, a warp per row: its lanes take the splits' LSE, then four columns each, eight
+// splits' loads at a time.
+template <int D>
+__global__ void __launch_bounds__(128) window_join_kernel(const float* __restrict__ o_part,
+                                                          const float* __restrict__ lse_part, int n_splits,
+                                                          long long rows, __nv_bfloat16* __restrict__ out,
+                                                          float* __restrict__ lse) {
+  static_assert(kMaxSplits <= 64, "two splits per lane");
+  const int lane = threadIdx.x & 31;
+  const long long r = (static_cast<long long>(blockIdx.x) * 128 + threadIdx.x) >> 5;
+  if (r >= rows) return;
+  const float l0 = lane < n_splits ? lse_part[lane * rows + r] : -INFINITY;
+  const float l1 = lane + 32 < n_splits ? lse_part[(lane + 32) * rows + r] : -INFINITY;
+  float m = fmaxf(l0, l1);
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const float ms = m == -INFINITY ? 0.f : m;
+  const float w0 = expf(l0 - ms), w1 = expf(l1 - ms);
+  float z = w0 + w1;
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) z += __shfl_xor_sync(0xffffffffu, z, d);
+  const bool mine = lane * 4 < D;
+  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < n_splits; s0 += 8) {
+    float4 p[8];
+#pragma unroll
+    for (int y = 0; y < 8; ++y)
+      p[y] = mine && s0 + y < n_splits ? *reinterpret_cast<const float4*>(o_part + ((s0 + y) * rows + r) * D + lane * 4)
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+      const float w = __shfl_sync(0xffffffffu, s0 + y < 32 ? w0 : w1, (s0 + y) & 31);
+      t.x += w * p[y].x;
+      t.y += w * p[y].y;
+      t.z += w * p[y].z;
+      t.w += w * p[y].w;
+    }
+  }
+  const float inv = z > 0.f ? 1.f / z : 0.f;
+  if (mine) {
+    uint2 pk;
+    pk.x = pack_bf16x2(t.x * inv, t.y * inv);
+    pk.y = pack_bf16x2(t.z * inv, t.w * inv);
+    *reinterpret_cast<uint2*>(out + r * D + lane * 4) = pk;
+  }
+  if (lane == 0) lse[r] = z > 0.f ? m + logf(z) : -INFINITY;
+}
+
 struct DecPlan {
-  int row_tiles, n_splits;
+  int rt, row_blocks, n_splits, cluster;
   size_t ws;
 };
 
-// Splits: as many as fill every SM twice, none shorter than 64 keys per warp.
+// Splits: as many as fill the SMs (two CTAs each with one row tile a stream, one with two), none
+// shorter than a step per stream. Up to 8 make a cluster of a power of two. More, or a number that
+// is none, pay where rounding down would cost more than the partials' round trip and second launch
+// (about 5 us): from splits of 2048 keys on.
 DecPlan plan(int N, int n, int cap, int Hq, int Hkv, int D, int window, int sinks) {
   DecPlan p{};
-  p.row_tiles = (n * (Hq / Hkv) + 15) / 16;
+  const int rows = n * (Hq / Hkv);
+  p.rt = rows > 16 ? 2 : 1;
+  p.row_blocks = (rows + 16 * p.rt - 1) / (16 * p.rt);
   const long long most = static_cast<long long>(window) + n - 1 + sinks;
   const long long keys = most < cap ? most : cap;
-  const long long blocks = static_cast<long long>(N) * Hkv * p.row_tiles;
-  long long s = (2LL * kSms) / blocks;
-  const long long by_keys = keys / (64 * kWarps);
+  const long long blocks = static_cast<long long>(N) * Hkv * p.row_blocks;
+  long long s = (p.rt == 1 ? 2LL : 1LL) * kSms / blocks;
+  const int step = 16 * p.rt * kStreams;
+  const long long by_keys = (keys + step - 1) / step;
   if (s > by_keys) s = by_keys;
   if (s > kMaxSplits) s = kMaxSplits;
   if (s < 1) s = 1;
+  int c = 1;
+  while (2 * c <= s && 2 * c <= kMaxCluster) c *= 2;
+  p.cluster = 1;
+  if (c == s || keys / c < 2048) s = p.cluster = c;
   p.n_splits = static_cast<int>(s);
-  const size_t rows = static_cast<size_t>(N) * n * Hq;
-  p.ws = kStatusBytes + (p.n_splits > 1 ? p.n_splits * rows * (4 * static_cast<size_t>(D) + 4) : 0);
+  const size_t all = static_cast<size_t>(N) * n * Hq;
+  p.ws = kStatusBytes + (p.n_splits > p.cluster ? p.n_splits * all * (4 * static_cast<size_t>(D) + 4) : 0);
   return p;
+}
+
+template <int D, int kRt>
+cudaError_t launch_dec(const DecArgs& a, unsigned blocks, cudaStream_t st) {
+  using C = DecCfg<D, kRt>;
+  static_assert(C::kSmemBytes <= 227 * 1024, "shared memory budget");
+  cudaError_t e = cudaFuncSetAttribute(window_decode_kernel<D, kRt>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(a.cluster);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, window_decode_kernel<D, kRt>, a);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_join(const DecArgs& a, long long rows, cudaStream_t st) {
+  window_join_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(a.o_part, a.lse_part, a.n_splits, rows,
+                                                                            a.out, a.lse);
+  note_launch();
+  return cudaGetLastError();
 }
 
 int check(int N, int n, int cap, int Hq, int Hkv, int D, int window, int sinks) {
@@ -348,27 +517,19 @@ extern "C" int usp_window_attn_decode(const void* q, const void* k_cache, const 
   a.W = window;
   a.ns = sinks;
   a.n_splits = p.n_splits;
-  a.row_tiles = p.row_tiles;
+  a.cluster = p.cluster;
+  a.row_blocks = p.row_blocks;
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
   const long long rows = static_cast<long long>(N) * n * Hq;
   a.o_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
   a.lse_part = a.o_part + static_cast<size_t>(p.n_splits) * rows * D;
-  const long long blocks = static_cast<long long>(N) * Hkv * p.row_tiles * p.n_splits;
+  const long long blocks = static_cast<long long>(N) * Hkv * p.row_blocks * p.n_splits;
   if (blocks > 0x7FFFFFFFLL) return record_error(USP_ERR_UNSUPPORTED, "too many rows");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (D == 128) {
-    e = cudaFuncSetAttribute(window_decode_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecCfg<128>::kSmemBytes);
-    if (e == cudaSuccess) window_decode_kernel<128><<<static_cast<unsigned>(blocks), kThreads, DecCfg<128>::kSmemBytes, st>>>(a);
-  } else {
-    e = cudaFuncSetAttribute(window_decode_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecCfg<64>::kSmemBytes);
-    if (e == cudaSuccess) window_decode_kernel<64><<<static_cast<unsigned>(blocks), kThreads, DecCfg<64>::kSmemBytes, st>>>(a);
-  }
-  if (e == cudaSuccess) {
-    note_launch();
-    e = cudaGetLastError();
-  }
-  if (e == cudaSuccess && p.n_splits > 1)
-    e = launch_lse_merge(a.o_part, a.lse_part, p.n_splits, rows, D, out, 0, lse, st);
+  const unsigned nb = static_cast<unsigned>(blocks);
+  cudaError_t e = D == 128 ? (p.rt == 1 ? launch_dec<128, 1>(a, nb, st) : launch_dec<128, 2>(a, nb, st))
+                           : (p.rt == 1 ? launch_dec<64, 1>(a, nb, st) : launch_dec<64, 2>(a, nb, st));
+  if (e == cudaSuccess && p.n_splits > p.cluster)
+    e = D == 128 ? launch_join<128>(a, rows, st) : launch_join<64>(a, rows, st);
   return e == cudaSuccess ? USP_OK : record_error(USP_ERR_CUDA, "window decode launch: %s", cudaGetErrorString(e));
 }

@@ -236,6 +236,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return x;
     };
+    // X = A B^T of 128 rows and the first `keys` rows of B (128; 16 or 32 in a narrow tile)
+    auto xt = [&](uint32_t acc, uint64_t a0, uint64_t b0, int keys) {
+      auto go = [&](uint32_t idesc) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * C::kPanelBytes + (kk & 3) * 32) >> 4;
+          umma_bf16_w(acc, a0 + off, b0 + off, idesc, kk > 0 ? 1u : 0u);
+        }
+      };
+      if (keys == kBN)
+        go(idesc_bf16_f32(128, 128, 0, 0));
+      else
+        go(idesc_bf16_f32(128, keys, 0, 0));
+    };
     auto issue_s = [&](const Cursor& c) -> bool {  // S into buffer n & 1
       if (c.it == 0 && !mbar_wait_w(&bars->q_full, c.item & 1, w, kSiteQ)) return false;
       if (!mbar_wait_w(&bars->k_full[c.n % C::kKSt], (c.n / C::kKSt) & 1, w, kSiteK)) return false;
@@ -243,12 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (c.n >= 2 && !mbar_wait_w(&bars->dq_done[c.n & 1], ((c.n - 2) >> 1) & 1, w, kSiteDqDone)) return false;
       tc_fence_after();
       const uint64_t kd = dK0 + (((c.n % C::kKSt) * C::kTileBytes) >> 4);
-      const uint32_t idesc = idesc_bf16_f32(128, c.width(), 0, 0);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = ((kk >> 2) * C::kPanelBytes + (kk & 3) * 32) >> 4;
-        umma_bf16_w(tmem + col_s(c.n & 1), dQ0 + off, kd + off, idesc, kk > 0 ? 1u : 0u);
-      }
+      xt(tmem + col_s(c.n & 1), dQ0, kd, c.width());
       umma_commit_w(&bars->s_full[c.n & 1]);
       if (c.last()) umma_commit_w(&bars->q_empty);
       issued_any = true;
@@ -260,12 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (c.n >= 1 && !mbar_wait_w(&bars->dp_free, (c.n - 1) & 1, w, kSiteDpFree)) return false;
       tc_fence_after();
       const uint64_t vd = dV0 + (((c.n % C::kVSt) * C::kTileBytes) >> 4);
-      const uint32_t idesc = idesc_bf16_f32(128, c.width(), 0, 0);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = ((kk >> 2) * C::kPanelBytes + (kk & 3) * 32) >> 4;
-        umma_bf16_w(tmem + kColDP, dDO0 + off, vd + off, idesc, kk > 0 ? 1u : 0u);
-      }
+      xt(tmem + kColDP, dDO0, vd, c.width());
       umma_commit_w(&bars->dp_full);
       umma_commit_w(&bars->v_empty[c.n % C::kVSt]);
       if (c.last()) umma_commit_w(&bars->do_empty);
@@ -276,12 +280,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint64_t kd = dKmn + (((c.n % C::kKSt) * C::kTileBytes) >> 4);
       const int steps = c.width() / 16;  // 1, 2 or 8
-#pragma unroll
-      for (int kk = 0; kk < kBN / 16; ++kk) {
-        if (kk >= steps) break;
+      auto step = [&](int kk) {
         const uint32_t pcol = col_s(c.n & 1) + (kk < 4 ? 0u : 64u) + (kk & 3) * 8;
         umma_bf16_tmem_a_w(tmem + kColDQ, tmem + pcol, kd + ((kk * 16 * 128) >> 4), kIdKM,
                            (c.it > 0 || kk > 0) ? 1u : 0u);
+      };
+      if (steps == kBN / 16) {
+#pragma unroll
+        for (int kk = 0; kk < kBN / 16; ++kk) step(kk);
+      } else {
+#pragma unroll 1
+        for (int kk = 0; kk < steps; ++kk) step(kk);
       }
       umma_commit_w(&bars->dq_done[c.n & 1]);
       umma_commit_w(&bars->k_empty[c.n % C::kKSt]);
@@ -357,30 +366,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t cS = col_s(n & 1);
         const int k0 = kr.base(it), width = kr.width(it);
         const bool whole = k0 >= first_all && k0 + kBN - 1 <= x.q0;
+        const bool used = cbase < width;  // a narrow tile has the first 32 columns at most: warpgroup 0, half 0
+        // all of this thread's dP first, so that the next tile's dP can start while this one is worked on
+        uint32_t rp[2][32];
+        if (used) {
+          tmem_ld32(trow + kColDP + cbase, rp[0]);
+          if (width == kBN) tmem_ld32(trow + kColDP + cbase + 32, rp[1]);
+          tmem_ld_wait();
+          reg_fence32(rp[0]);
+          reg_fence32(rp[1]);
+        }
+        tc_fence_before();
+        mbar_arrive_warp(&bars->dp_free);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int c0 = cbase + half * 32;
-          uint32_t rs[32], rp[32];
-          const bool used = c0 < width;  // a narrow tile has the first 32 columns at most
-          if (used) {
-            tmem_ld32(trow + cS + c0, rs);
-            tmem_ld32(trow + kColDP + c0, rp);
-            tmem_ld_wait();
-            reg_fence32(rs);
-            reg_fence32(rp);
-          }
-          if (half == 1) {  // every dP column of this thread has been read
-            tc_fence_before();
-            mbar_arrive_warp(&bars->dp_free);
-          }
-          if (!used) continue;
+          if (c0 >= width) break;
+          uint32_t rs[32];
+          tmem_ld32(trow + cS + c0, rs);
+          tmem_ld_wait();
+          reg_fence32(rs);
           if (!whole) {
             const uint32_t vis = visible_bits(span, kr.kr, kr.pass_it(it), k0, c0);
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (!((vis >> c) & 1u)) {
                 rs[c] = 0xFF800000u;
-                rp[c] = 0u;  // columns past a narrow tile's width hold what an earlier tile left
+                rp[half][c] = 0u;  // columns past a narrow tile's width hold what an earlier tile left
               }
           }
           uint32_t dk[16];
@@ -389,7 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 32; c += 2) {
               const float2 y = ffma2(make_float2(__uint_as_float(rs[c]), __uint_as_float(rs[c + 1])), sl2, nl2);
               const float2 pv = make_float2(ex2_approx(y.x), ex2_approx(y.y));  // -inf -> 0
-              const float2 ds = fmul2(pv, fadd2(make_float2(__uint_as_float(rp[c]), __uint_as_float(rp[c + 1])), nd2));
+              const float2 ds =
+                  fmul2(pv, fadd2(make_float2(__uint_as_float(rp[half][c]), __uint_as_float(rp[half][c + 1])), nd2));
               res2 = fadd2(res2, ds);
               dk[c >> 1] = pack_bf16x2(ds.x, ds.y);
             }

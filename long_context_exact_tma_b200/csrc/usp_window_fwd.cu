@@ -206,8 +206,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dQ0 = sdesc_sw128(smem_addr(sQ), 16, 1024);
     const uint64_t dK0 = sdesc_sw128(smem_addr(sK), 16, 1024);
     const uint64_t dV0 = sdesc_sw128(smem_addr(sV), C::kPanelBytes, 1024);
-    auto issue_s = [&](int t, int ks, int keys) {  // S_t = Q_t K^T, the first `keys` keys of stage ks
-      const uint32_t idesc = idesc_bf16_f32(kBM, keys, 0, 0);
+    // S_t = Q_t K^T with stage ks; the narrow form takes the stage's first `keys` (16 or 32)
+    auto issue_s_as = [&](int t, int ks, uint32_t idesc) {
       const uint64_t qd = dQ0 + ((t * C::kTileBytes) >> 4), kd = dK0 + ((ks * C::kTileBytes) >> 4);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
@@ -215,6 +215,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_bf16_w(tmem + col_s(t), qd + off, kd + off, idesc, kk > 0 ? 1u : 0u);
       }
       umma_commit_w(&bars->s_full[t]);
+    };
+    auto issue_s = [&](int t, int ks, int keys) {
+      if (keys == kBN)
+        issue_s_as(t, ks, idesc_bf16_f32(kBM, kBN, 0, 0));
+      else
+        issue_s_as(t, ks, idesc_bf16_f32(kBM, keys, 0, 0));
     };
     auto run_of = [&](int idx) {
       const Item x = item_of(g, idx);
@@ -246,17 +252,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto issue_pv = [&](int t) -> bool {  // in two halves of 64 keys, each as soon as its P is in TMEM
           if (!mbar_wait_w(&bars->p_half[t], n & 1, w, kSiteP)) return false;
           tc_fence_after();
+          if (pv_steps == kBN / 16) {
 #pragma unroll
-          for (int kk = 0; kk < kBN / 32; ++kk)
-            if (kk < pv_steps)
+            for (int kk = 0; kk < kBN / 32; ++kk)
               umma_bf16_tmem_a_w(tmem + col_o(t), tmem + col_s(t) + kk * 8, vd + ((kk * 16 * 128) >> 4), kIdescPV,
                                  (it > 0 || kk > 0) ? 1u : 0u);
-          if (!mbar_wait_w(&bars->p_full[t], n & 1, w, kSiteP)) return false;
-          tc_fence_after();
-          if (pv_steps == kBN / 16) {
+            if (!mbar_wait_w(&bars->p_full[t], n & 1, w, kSiteP)) return false;
+            tc_fence_after();
 #pragma unroll
             for (int kk = kBN / 32; kk < kBN / 16; ++kk)
               umma_bf16_tmem_a_w(tmem + col_o(t), tmem + col_s(t) + kk * 8, vd + ((kk * 16 * 128) >> 4), kIdescPV, 1u);
+          } else {  // a narrow tile: one or two steps, all of its P handed over at once
+#pragma unroll 1
+            for (int kk = 0; kk < pv_steps; ++kk)
+              umma_bf16_tmem_a_w(tmem + col_o(t), tmem + col_s(t) + kk * 8, vd + ((kk * 16 * 128) >> 4), kIdescPV,
+                                 (it > 0 || kk > 0) ? 1u : 0u);
+            if (!mbar_wait_w(&bars->p_full[t], n & 1, w, kSiteP)) return false;
           }
           umma_commit_w(&bars->pv_done[t]);
           if (t == 1) umma_commit_w(&bars->v_empty[s]);
@@ -308,54 +319,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int h = x.h + t * x.dh, q0 = x.q0 + t * x.dq;
       const int i = q0 + row;
       const bool store = i < g.S;
-      const RowSpan span = row_span(g, i);
-      // the first key that every row of the tile sees, and the row up to which every row sees
+      // the row's document start; one that no key reaches for a row past the end
+      const int lo = store ? win_lo(g, i) : 1 << 30;
+      // the first key that every row of the tile sees
       const int q_last = min(q0 + kBM, g.S) - 1;
       const int first_all = q_last < q0 ? INT_MAX : max(win_lo(g, q_last), q_last - g.W + 1);
       // l_run: sum of the fp32 weights (LSE); lb_run: sum of the bf16-rounded weights that the
       // PV product takes (O's divisor, so that O stays a convex combination of V rows)
       float m_use = -INFINITY, l_run = 0.f, lb_run = 0.f;
-      for (int it = 0; it < kr.nt; ++it, ++n) {
+      const int n0 = n;
+      const int n_end = n + kr.nt;
+      const float2 sl2 = make_float2(g.scale_log2, g.scale_log2);
+      if (kr.n_s && kr.cols <= 32) {
+        // a narrow sink tile, the item's first: one group of 32 columns, no O to rescale yet
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[t], n & 1, w, kSiteS));
         if (!ok) break;
         tc_fence_after();
-        const int k0 = kr.base(it);
-        const float2 sl2 = make_float2(g.scale_log2, g.scale_log2);
-        if (kr.sink(it) && kr.cols <= 32) {
-          // a narrow sink tile, always an item's first: one group of 32 columns, no O to rescale yet
-          uint32_t r[32];
-          tmem_ld32(trow + cS, r);
-          tmem_ld_wait();
-          reg_fence32(r);
-          const uint32_t vis = visible_bits(span, kr, it, k0, 0);
-          float mx = -INFINITY;
+        uint32_t r[32];
+        tmem_ld32(trow + cS, r);
+        tmem_ld_wait();
+        reg_fence32(r);
+        const uint32_t vis = bits_between(lo - kr.lo, min(min(lo + g.ns, i + 1), kr.w0 * kBN) - kr.lo, 0);
+        float mx = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            if (!((vis >> c) & 1u)) r[c] = 0xFF800000u;
-            mx = fmaxf(mx, __uint_as_float(r[c]));
-          }
-          m_use = mx * g.scale_log2;
-          const float m_safe = m_use == -INFINITY ? 0.f : m_use;
-          float2 acc = make_float2(0.f, 0.f), accb = acc;
-          uint32_t pk[16];
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float2 y = ffma2(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sl2,
-                                   make_float2(-m_safe, -m_safe));
-            const float2 pv = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-            acc = fadd2(acc, pv);
-            pk[c >> 1] = pack_bf16x2(pv.x, pv.y);
-            accb = add_bf16x2_f32(accb, pk[c >> 1]);
-          }
-          l_run = acc.x + acc.y;
-          lb_run = accb.x + accb.y;
-          tmem_st16(trow + cS, pk);
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive_warp(&bars->p_half[t]);
-          mbar_arrive_warp(&bars->p_full[t]);
-          continue;
+        for (int c = 0; c < 32; ++c) {
+          if (!((vis >> c) & 1u)) r[c] = 0xFF800000u;
+          mx = fmaxf(mx, __uint_as_float(r[c]));
         }
+        m_use = mx * g.scale_log2;
+        const float m_safe = m_use == -INFINITY ? 0.f : m_use;
+        float2 acc = make_float2(0.f, 0.f), accb = acc;
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          const float2 y = ffma2(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sl2,
+                                 make_float2(-m_safe, -m_safe));
+          const float2 pv = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+          acc = fadd2(acc, pv);
+          pk[c >> 1] = pack_bf16x2(pv.x, pv.y);
+          accb = add_bf16x2_f32(accb, pk[c >> 1]);
+        }
+        l_run = acc.x + acc.y;
+        lb_run = accb.x + accb.y;
+        tmem_st16(trow + cS, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(&bars->p_half[t]);
+        mbar_arrive_warp(&bars->p_full[t]);
+        ++n;
+      }
+      // keys of the next tile: a wide sink tile's, or the window's first
+      int k0 = kr.n_s && kr.cols > 32 ? kr.lo : kr.w0 * kBN;
+      const int w0 = kr.w0 * kBN;
+      for (; n < n_end; ++n) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[t], n & 1, w, kSiteS));
+        if (!ok) break;
+        tc_fence_after();
         uint32_t r0[32], r1[32], r2[32], r3[32];
         tmem_ld32(trow + cS + 0, r0);
         tmem_ld32(trow + cS + 32, r1);
@@ -367,8 +386,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         reg_fence32(r2);
         reg_fence32(r3);
         if (!(k0 >= first_all && k0 + kBN - 1 <= q0)) {  // not visible as a whole: -inf where it is not
+          const int first = k0 < w0 ? INT_MAX : max(lo, i - g.W + 1);
+          const int sink_end = min(min(lo + g.ns, i + 1), k0 < w0 ? w0 : INT_MAX);
           auto hide = [&](uint32_t (&r)[32], int c0) {
-            const uint32_t vis = visible_bits(span, kr, it, k0, c0);
+            const uint32_t vis = bits_between(first - k0, i + 1 - k0, c0) | bits_between(lo - k0, sink_end - k0, c0);
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (!((vis >> c) & 1u)) r[c] = 0xFF800000u;
@@ -400,9 +421,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           m_use = m_tile;
         }
         const float m_safe = m_use == -INFINITY ? 0.f : m_use;
-        float2 acc[4], accb[4];
+        float2 acc[2], accb[2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[q] = accb[q] = make_float2(0.f, 0.f);
+        for (int q = 0; q < 2; ++q) acc[q] = accb[q] = make_float2(0.f, 0.f);
         const float2 nm = make_float2(-m_safe, -m_safe);
         auto emit = [&](const uint32_t (&r)[32], uint32_t col) {
           uint32_t pk[16];
@@ -410,9 +431,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 32; c += 2) {
             const float2 y = ffma2(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sl2, nm);
             const float2 pv = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-            acc[(c >> 1) & 3] = fadd2(acc[(c >> 1) & 3], pv);
+            acc[(c >> 1) & 1] = fadd2(acc[(c >> 1) & 1], pv);
             pk[c >> 1] = pack_bf16x2(pv.x, pv.y);
-            accb[(c >> 1) & 3] = add_bf16x2_f32(accb[(c >> 1) & 3], pk[c >> 1]);
+            accb[(c >> 1) & 1] = add_bf16x2_f32(accb[(c >> 1) & 1], pk[c >> 1]);
           }
           tmem_st16(trow + cS + col, pk);
         };
@@ -420,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         emit(r1, 16);
         // the previous PV has landed (S_t is issued behind it): O_t can be rescaled in place
         // before the first half of P is handed over
-        if (it > 0 && __any_sync(0xffffffffu, bump)) {
+        if (n > n0 && __any_sync(0xffffffffu, bump)) {
 #pragma unroll
           for (int c0 = 0; c0 < D; c0 += 32) {
             uint32_t o[32];
@@ -437,14 +458,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_warp(&bars->p_half[t]);
         emit(r2, 32);
         emit(r3, 48);
-        const float rs = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y) + (acc[2].x + acc[2].y) + (acc[3].x + acc[3].y);
-        const float rsb =
-            (accb[0].x + accb[0].y) + (accb[1].x + accb[1].y) + (accb[2].x + accb[2].y) + (accb[3].x + accb[3].y);
+        const float rs = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+        const float rsb = (accb[0].x + accb[0].y) + (accb[1].x + accb[1].y);
         l_run = l_run * alpha + rs;
         lb_run = lb_run * alpha + rsb;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive_warp(&bars->p_full[t]);
+        k0 = k0 < w0 ? w0 : k0 + kBN;
       }
       // ------------------------------------------------------------ epilogue
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[t], (n - 1) & 1, w, kSiteO));
