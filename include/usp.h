@@ -443,8 +443,9 @@ int usp_window_attn_bwd(const void* q, const void* k, const void* v, const void*
  *                taken as the nearer end); rows past lens are never read
  *   out          [N][n][Hq][D] bf16;  lse [N][n][Hq] fp32. A token at a negative
  *                position (lens[s] < n) sees nothing: out = 0, lse = -inf.
- *   workspace    usp_window_decode_workspace_size(...) bytes (fp32 partials of the
- *                splits; no status is kept: the kernels wait for nothing)
+ *   workspace    usp_window_decode_workspace_size(...) bytes: fp32 partials of the
+ *                splits (no status is kept: the kernels wait for nothing). A size of
+ *                256 means that there are none; workspace may then be NULL.
  */
 #define USP_WINDOW_MAX_NEW 16
 size_t usp_window_decode_workspace_size(int N, int n, int cap, int Hq, int Hkv, int D, int window, int sinks);

@@ -277,46 +277,64 @@ def bwd_preprocess(out: torch.Tensor, dO: torch.Tensor, stream=None) -> torch.Te
 _HERE = contextlib.nullcontext()
 
 
-def _check(name: str, t: torch.Tensor, ref: torch.Tensor, dtype, shape=None, contiguous=True) -> torch.Tensor:
-    """An argument of the calls below: a tensor of ref's device with this type and shape."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != ref.device:
+# The checks below are on the path of calls that take a few microseconds: device
+# numbers instead of device objects, one comparison per property.
+def _refuse(name: str, t, dev: int, dtype, shape, contiguous: bool):
+    """Says what is wrong with an argument that one of the calls below has turned down."""
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0 or t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on the device of the first one")
     if t.dtype != dtype:
         raise TypeError(f"{name} must have dtype {dtype}, not {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _on(ref: torch.Tensor, stream, *inputs):
-    """(context, raw stream) of a call: the current stream of ref's device, or the given one. What the
-    call allocates inside the context belongs to that stream; with a given stream the inputs are kept
-    from the allocator until its work on them is done."""
-    index = ref.device.index
+def _check(name: str, t, dev: int, dtype, shape=None, contiguous: bool = True) -> None:
+    """An argument of the calls below: a tensor of CUDA device `dev` with this type and shape."""
+    if (not isinstance(t, torch.Tensor) or t.get_device() != dev or dev < 0 or t.dtype is not dtype
+            or (shape is not None and t.shape != shape) or (contiguous and not t.is_contiguous())):
+        _refuse(name, t, dev, dtype, shape, contiguous)
+
+
+def _on(dev: int, stream, *inputs):
+    """(context, raw stream) of a call on CUDA device `dev`: the device's current stream, or the given
+    one. What the call allocates inside the context belongs to that stream; with a given stream the inputs
+    are kept from the allocator until its work on them is done."""
     if stream is not None:
-        s = torch.cuda.ExternalStream(stream, ref.device) if isinstance(stream, int) else stream
-        if s.device != ref.device:
+        s = torch.cuda.ExternalStream(stream, dev) if isinstance(stream, int) else stream
+        if s.device.index != dev:
             raise ValueError("the stream is of another device than the tensors")
         for t in inputs:
             if t is not None:
                 t.record_stream(s)
         return torch.cuda.stream(s), s.cuda_stream
     # (torch.cuda.current_stream() builds an object at ten times the price)
-    return (_HERE if index == torch._C._cuda_getDevice() else torch.cuda.device(ref.device),
-            torch._C._cuda_getCurrentRawStream(index))
+    return (_HERE if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev),
+            torch._C._cuda_getCurrentRawStream(dev))
 
 
-def _scratch(ws, nbytes: int, ref: torch.Tensor) -> torch.Tensor:
+def _scratch(ws, nbytes: int, ref: torch.Tensor, dev: int) -> torch.Tensor:
     """The given workspace, or a new one (the calls below clear what they need of it)."""
     if ws is None:
         return ref.new_empty(nbytes, dtype=torch.uint8)
-    return _check("ws", ws, ref, torch.uint8)
+    _check("ws", ws, dev, torch.uint8)
+    return ws
 
 
-def _new(t, name: str, shape, dtype, ref: torch.Tensor) -> torch.Tensor:
-    return ref.new_empty(shape, dtype=dtype) if t is None else _check(name, t, ref, dtype, shape)
+def _like(t, name: str, ref: torch.Tensor, dev: int) -> torch.Tensor:
+    """The given output, or a new one like ref."""
+    if t is None:
+        return torch.empty_like(ref)
+    _check(name, t, dev, ref.dtype, ref.shape)
+    return t
+
+
+def _lse_of(t, q: torch.Tensor, shape, dev: int) -> torch.Tensor:
+    if t is None:
+        return q.new_empty(shape, dtype=torch.float32)
+    _check("lse", t, dev, torch.float32, shape)
+    return t
 
 
 def _window_geometry(q, k, v, window, sinks, cu_seqlens):
@@ -324,18 +342,26 @@ def _window_geometry(q, k, v, window, sinks, cu_seqlens):
         raise ValueError("q must be [B, S, Hq, D] and k, v [B, S, Hkv, D]")
     B, S, Hq, D = q.shape
     Hkv = k.shape[2]
-    _check("q", q, q, torch.bfloat16)
-    _check("k", k, q, torch.bfloat16, (B, S, Hkv, D))
-    _check("v", v, q, torch.bfloat16, (B, S, Hkv, D))
+    dev = q.get_device()
+    _check("q", q, dev, torch.bfloat16)
+    _check("k", k, dev, torch.bfloat16, (B, S, Hkv, D))
+    _check("v", v, dev, torch.bfloat16, (B, S, Hkv, D))
     n_docs = 0
     if cu_seqlens is not None:
-        _check("cu_seqlens", cu_seqlens, q, torch.int32)
+        _check("cu_seqlens", cu_seqlens, dev, torch.int32)
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens must be [n_docs + 1]")
         n_docs = cu_seqlens.numel() - 1
-    return (B, S, Hq, Hkv, D, int(window), int(sinks)), n_docs
+    return (B, S, Hq, Hkv, D, int(window), int(sinks)), n_docs, dev
 
 
+def _ws_bytes(n: int, what: str, *geometry) -> int:
+    if n == 0:
+        raise B_.UspError(B_.USP_ERR_UNSUPPORTED, f"{what}{geometry}: {B_.usp_last_error()}")
+    return n
+
+
+# (pure functions of the sizes)
 @functools.lru_cache(maxsize=256)
 def _window_ws(*geometry) -> int:
     return _ws_bytes(B_.usp_window_workspace_size(*geometry), "window attention", *geometry)
@@ -346,25 +372,19 @@ def _decode_ws(*geometry) -> int:
     return _ws_bytes(B_.usp_window_decode_workspace_size(*geometry), "window decode", *geometry)
 
 
-def _ws_bytes(n: int, what: str, *geometry) -> int:
-    if n == 0:
-        raise B_.UspError(B_.USP_ERR_UNSUPPORTED, f"{what}{geometry}: {B_.usp_last_error()}")
-    return n
-
-
 def window_attn_fwd(q, k, v, window: int, sinks: int = 0, cu_seqlens=None, ws=None, out=None, lse=None, stream=None,
                     check_status: bool = False):
     """Causal attention with a sliding window and sinks over global-layout q [B, S, Hq, D], k/v
     [B, S, Hkv, D] (bf16): query i sees its own and the window - 1 keys before it, and the first
     `sinks` keys; with cu_seqlens ([n_docs + 1] int32, CUDA) all within its document. Returns
     (out bf16 like q, lse fp32 [B, S, Hq]). Elements must be finite, hidden ones too."""
-    geo, n_docs = _window_geometry(q, k, v, window, sinks, cu_seqlens)
+    geo, n_docs, dev = _window_geometry(q, k, v, window, sinks, cu_seqlens)
     need = _window_ws(*geo, n_docs, 0)
-    ctx, st = _on(q, stream, q, k, v, cu_seqlens, ws, out, lse)
+    ctx, st = _on(dev, stream, q, k, v, cu_seqlens, ws, out, lse)
     with ctx:
-        out = _new(out, "out", q.shape, torch.bfloat16, q)
-        lse = _new(lse, "lse", q.shape[:-1], torch.float32, q)
-        ws = _scratch(ws, need, q)
+        out = _like(out, "out", q, dev)
+        lse = _lse_of(lse, q, geo[:3], dev)
+        ws = _scratch(ws, need, q, dev)
         B_.usp_window_attn_fwd(q, k, v, out, lse, *geo, cu_seqlens, n_docs, ws, ws.numel(), st)
         if check_status:
             check_workspace(ws, st)
@@ -374,17 +394,17 @@ def window_attn_fwd(q, k, v, window: int, sinks: int = 0, cu_seqlens=None, ws=No
 def window_attn_bwd(q, k, v, out, lse, dO, window: int, sinks: int = 0, cu_seqlens=None, ws=None, dq=None, dk=None,
                     dv=None, stream=None, check_status: bool = False):
     """Backward of window_attn_fwd from its out and lse; returns (dQ, dK, dV) in bf16, like q, k, v."""
-    geo, n_docs = _window_geometry(q, k, v, window, sinks, cu_seqlens)
-    _check("out", out, q, torch.bfloat16, q.shape)
-    _check("dO", dO, q, torch.bfloat16, q.shape)
-    _check("lse", lse, q, torch.float32, q.shape[:-1])
+    geo, n_docs, dev = _window_geometry(q, k, v, window, sinks, cu_seqlens)
+    _check("out", out, dev, torch.bfloat16, q.shape)
+    _check("dO", dO, dev, torch.bfloat16, q.shape)
+    _check("lse", lse, dev, torch.float32, geo[:3])
     need = _window_ws(*geo, n_docs, 1)
-    ctx, st = _on(q, stream, q, k, v, out, lse, dO, cu_seqlens, ws, dq, dk, dv)
+    ctx, st = _on(dev, stream, q, k, v, out, lse, dO, cu_seqlens, ws, dq, dk, dv)
     with ctx:
-        dq = _new(dq, "dq", q.shape, torch.bfloat16, q)
-        dk = _new(dk, "dk", k.shape, torch.bfloat16, q)
-        dv = _new(dv, "dv", v.shape, torch.bfloat16, q)
-        ws = _scratch(ws, need, q)
+        dq = _like(dq, "dq", q, dev)
+        dk = _like(dk, "dk", k, dev)
+        dv = _like(dv, "dv", v, dev)
+        ws = _scratch(ws, need, q, dev)
         B_.usp_window_attn_bwd(q, k, v, out, lse, dO, dq, dk, dv, *geo, cu_seqlens, n_docs, ws, ws.numel(), st)
         if check_status:
             check_workspace(ws, st)
@@ -402,21 +422,24 @@ def window_attn_decode(q, k_cache, v_cache, lens, window: int, sinks: int = 0, w
         raise ValueError("q must be [N, n, Hq, D] and the caches [N, cap, Hkv, D]")
     N, n, Hq, D = q.shape
     cap, Hkv = k_cache.shape[1], k_cache.shape[2]
-    _check("q", q, q, torch.bfloat16)
-    _check("k_cache", k_cache, q, torch.bfloat16, (N, cap, Hkv, D), contiguous=False)
-    _check("v_cache", v_cache, q, torch.bfloat16, (N, cap, Hkv, D), contiguous=False)
-    _check("lens", lens, q, torch.int32, (N,))
+    dev = q.get_device()
+    _check("q", q, dev, torch.bfloat16)
+    _check("k_cache", k_cache, dev, torch.bfloat16, (N, cap, Hkv, D), contiguous=False)
+    _check("v_cache", v_cache, dev, torch.bfloat16, (N, cap, Hkv, D), contiguous=False)
+    _check("lens", lens, dev, torch.int32, (N,))
     ks, vs = k_cache.stride(), v_cache.stride()
     if ks[3] != 1 or vs[3] != 1:
         raise ValueError("the last dimension of the caches must be contiguous")
     geo = (N, n, cap, Hq, Hkv, D, int(window), int(sinks))
     need = _decode_ws(*geo)
-    ctx, st = _on(q, stream, q, k_cache, v_cache, lens, ws, out, lse)
+    ctx, st = _on(dev, stream, q, k_cache, v_cache, lens, ws, out, lse)
     with ctx:
-        out = _new(out, "out", q.shape, torch.bfloat16, q)
-        lse = _new(lse, "lse", q.shape[:-1], torch.float32, q)
-        ws = _scratch(ws, need, q)
-        B_.usp_window_attn_decode(q, k_cache, v_cache, lens, out, lse, *geo, ks[:3], vs[:3], ws, ws.numel(), st)
+        out = _like(out, "out", q, dev)
+        lse = _lse_of(lse, q, (N, n, Hq), dev)
+        # (the smallest size: the splits join in the launch itself and need none)
+        ws = _scratch(ws, need, q, dev) if ws is not None or need > 256 else None
+        B_.usp_window_attn_decode(q, k_cache, v_cache, lens, out, lse, *geo, ks[:3], vs[:3], ws,
+                                  0 if ws is None else ws.numel(), st)
     return out, lse
 
 
@@ -433,38 +456,46 @@ def rope_axes(xs, positions, inv_freq, axis, paired: bool = False, inverse: bool
     if not xs or len(xs) > B_.USP_MAX_ROPE_JOBS:
         raise ValueError(f"one to {B_.USP_MAX_ROPE_JOBS} tensors")
     x0 = xs[0]
+    dtype, dev = x0.dtype, x0.get_device()
     dt = _dt(x0)
-    if x0.dim() != 4:
-        raise ValueError("tensors must be [B, S, H, D]")
-    B, S, _, D = x0.shape
-    for x in xs:
-        if x.dim() != 4:
-            raise ValueError("tensors must be [B, S, H, D]")
-        _check("x", x, x0, x0.dtype, (B, S, x.shape[2], D), contiguous=False)
-    if positions.dtype not in (torch.int32, torch.int64):
-        raise TypeError("positions must be int32 or int64")
-    _check("positions", positions, x0, positions.dtype)
-    if positions.dim() != 3 or positions.shape[1:] != (B, S):
-        raise ValueError(f"positions must be [n_axes, {B}, {S}]")
-    for name, t, want in (("inv_freq", inv_freq, torch.float64), ("axis", axis, torch.int32)):
-        if t.device.type != "cpu" or t.dtype != want or t.dim() != 1 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous 1-D {want} tensor on the CPU")
-    if inv_freq.numel() != axis.numel():
-        raise ValueError("inv_freq and axis must have one entry per frequency")
     outs = ((outs,) if single else tuple(outs)) if outs is not None else (None,) * len(xs)
     if len(outs) != len(xs):
         raise ValueError("one output per tensor")
-    ctx, st = _on(x0, stream, positions, *xs, *outs)
+    if x0.dim() != 4:
+        raise ValueError("tensors must be [B, S, H, D]")
+    B, S, _, D = x0.shape
+    pos_type = positions.dtype
+    if pos_type is not torch.int64 and pos_type is not torch.int32:
+        raise TypeError("positions must be int32 or int64")
+    _check("positions", positions, dev, pos_type)
+    if positions.dim() != 3 or positions.shape[1] != B or positions.shape[2] != S:
+        raise ValueError(f"positions must be [n_axes, {B}, {S}]")
+    if inv_freq.get_device() >= 0 or inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous 1-D float64 tensor on the CPU")
+    if axis.get_device() >= 0 or axis.dtype is not torch.int32 or axis.dim() != 1 or not axis.is_contiguous():
+        raise ValueError("axis must be a contiguous 1-D int32 tensor on the CPU")
+    n_freq = inv_freq.numel()
+    if n_freq != axis.numel():
+        raise ValueError("inv_freq and axis must have one entry per frequency")
+    ctx, st = _on(dev, stream, positions, *xs, *outs)
     with ctx:
         ys, jobs = [], []
         for x, y in zip(xs, outs):
-            y = (torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None
-                 else _check("out", y, x0, x.dtype, x.shape, contiguous=False))
-            sx, sy = x.stride(), y.stride()
-            if D > 1 and (sx[3] != 1 or sy[3] != 1):
+            if x.dim() != 4:
+                raise ValueError("tensors must be [B, S, H, D]")
+            H = x.shape[2]
+            _check("x", x, dev, dtype, (B, S, H, D), contiguous=False)
+            sx = x.stride()
+            if y is None:
+                y = torch.empty_like(x, memory_format=torch.contiguous_format)
+                sy = (S * H * D, H * D, D, 1)
+            else:
+                _check("out", y, dev, dtype, (B, S, H, D), contiguous=False)
+                sy = y.stride()
+            if (sx[3] != 1 or sy[3] != 1) and D > 1:
                 raise ValueError("the last dimension must be contiguous")
             ys.append(y)
-            jobs.append((x, y, x.shape[2], sx[:3], sy[:3]))
-        B_.usp_rope_axes(jobs, B, S, D, 2 * inv_freq.numel(), dt, positions, 8 * positions.element_size(),
+            jobs.append((x, y, H, sx[:3], sy[:3]))
+        B_.usp_rope_axes(jobs, B, S, D, 2 * n_freq, dt, positions, 64 if pos_type is torch.int64 else 32,
                          positions.shape[0], inv_freq, axis, paired, inverse, st)
     return ys[0] if single else ys

@@ -502,7 +502,8 @@ extern "C" int usp_window_attn_decode(const void* q, const void* k_cache, const 
     if (s < 0 || s % 8) return record_error(USP_ERR_INVALID_ARG, "cache strides must be multiples of 8 elements");
   if (window > cap) window = cap;
   const DecPlan p = plan(N, n, cap, Hq, Hkv, D, window, sinks);
-  if (!workspace || ws_bytes < p.ws || (reinterpret_cast<uintptr_t>(workspace) & 15u))
+  const bool parts = p.n_splits > p.cluster;
+  if (parts && (!workspace || ws_bytes < p.ws || (reinterpret_cast<uintptr_t>(workspace) & 15u)))
     return record_error(USP_ERR_WORKSPACE, "workspace needs %zu bytes (got %zu)", p.ws, ws_bytes);
   DecArgs a{};
   a.q = static_cast<const __nv_bfloat16*>(q);
@@ -521,15 +522,17 @@ extern "C" int usp_window_attn_decode(const void* q, const void* k_cache, const 
   a.row_blocks = p.row_blocks;
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
   const long long rows = static_cast<long long>(N) * n * Hq;
-  a.o_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
-  a.lse_part = a.o_part + static_cast<size_t>(p.n_splits) * rows * D;
+  if (parts) {
+    a.o_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
+    a.lse_part = a.o_part + static_cast<size_t>(p.n_splits) * rows * D;
+  }
   const long long blocks = static_cast<long long>(N) * Hkv * p.row_blocks * p.n_splits;
   if (blocks > 0x7FFFFFFFLL) return record_error(USP_ERR_UNSUPPORTED, "too many rows");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const unsigned nb = static_cast<unsigned>(blocks);
   cudaError_t e = D == 128 ? (p.rt == 1 ? launch_dec<128, 1>(a, nb, st) : launch_dec<128, 2>(a, nb, st))
                            : (p.rt == 1 ? launch_dec<64, 1>(a, nb, st) : launch_dec<64, 2>(a, nb, st));
-  if (e == cudaSuccess && p.n_splits > p.cluster)
+  if (e == cudaSuccess && parts)
     e = D == 128 ? launch_join<128>(a, rows, st) : launch_join<64>(a, rows, st);
   return e == cudaSuccess ? USP_OK : record_error(USP_ERR_CUDA, "window decode launch: %s", cudaGetErrorString(e));
 }

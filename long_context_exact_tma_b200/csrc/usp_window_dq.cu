@@ -107,12 +107,17 @@ __device__ __forceinline__ DqRun run_of(const WinGeo& g, const Item& x) {
   return r;
 }
 
-// A key tile of the CTA's stream: which of which item, and where its barriers stand.
-struct Cursor {
-  int idx, it, item, n;  // work item, tile in it, item and tile of the stream
-  DqRun run;
-  __device__ __forceinline__ bool last() const { return it + 1 == run.nt; }
-  __device__ __forceinline__ int width() const { return run.width(it); }
+// A position in a ring of kN stages: the stage, and the parity of its current use.
+template <int kN>
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == kN) {
+      at = 0;
+      phase ^= 1u;
+    }
+  }
 };
 
 template <int D>
@@ -223,19 +228,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dK0 = sdesc_sw128(smem_addr(sK), 16, 1024), dV0 = sdesc_sw128(smem_addr(sV), 16, 1024);
     const uint64_t dKmn = sdesc_sw128(smem_addr(sK), C::kPanelBytes, 1024);
     bool issued_any = false;
-    auto next = [&](const Cursor& c) -> Cursor {  // the tile behind c (idx >= n_items: none)
-      Cursor x = c;
-      ++x.n;
-      if (c.last()) {
-        x.idx += stride;
-        x.it = 0;
-        ++x.item;
-        if (x.idx < a.n_items) x.run = run_of(g, item_of(g, x.idx));
-      } else {
-        ++x.it;
-      }
-      return x;
-    };
+    // The loop below is one warp's chain of dependent steps between the products, so it
+    // keeps its state in a few counters: ring positions of the K stage that S takes next
+    // and that dQ takes next, of the V stage that dP takes next, and the S buffers' turns.
+    Ring<C::kKSt> k_s, k_q;
+    Ring<C::kVSt> v_d;
+    uint32_t s_turn = 0, q_turn = 0;  // tiles whose S, dQ have been issued
+    uint32_t item = 0;
     // X = A B^T of 128 rows and the first `keys` rows of B (128; 16 or 32 in a narrow tile)
     auto xt = [&](uint32_t acc, uint64_t a0, uint64_t b0, int keys) {
       auto go = [&](uint32_t idesc) {
@@ -250,78 +249,91 @@ __global__ void __launch_bounds__(kThreads, 1)
       else
         go(idesc_bf16_f32(128, keys, 0, 0));
     };
-    auto issue_s = [&](const Cursor& c) -> bool {  // S into buffer n & 1
-      if (c.it == 0 && !mbar_wait_w(&bars->q_full, c.item & 1, w, kSiteQ)) return false;
-      if (!mbar_wait_w(&bars->k_full[c.n % C::kKSt], (c.n / C::kKSt) & 1, w, kSiteK)) return false;
+    auto issue_s = [&](int keys) -> bool {  // S into the buffer whose turn it is
+      if (!mbar_wait_w(&bars->k_full[k_s.at], k_s.phase, w, kSiteK)) return false;
       // dQ two tiles back has read its dS from the buffer
-      if (c.n >= 2 && !mbar_wait_w(&bars->dq_done[c.n & 1], ((c.n - 2) >> 1) & 1, w, kSiteDqDone)) return false;
+      if (s_turn >= 2 && !mbar_wait_w(&bars->dq_done[s_turn & 1], ((s_turn - 2) >> 1) & 1, w, kSiteDqDone)) return false;
       tc_fence_after();
-      const uint64_t kd = dK0 + (((c.n % C::kKSt) * C::kTileBytes) >> 4);
-      xt(tmem + col_s(c.n & 1), dQ0, kd, c.width());
-      umma_commit_w(&bars->s_full[c.n & 1]);
-      if (c.last()) umma_commit_w(&bars->q_empty);
+      xt(tmem + col_s(s_turn & 1), dQ0, dK0 + ((k_s.at * C::kTileBytes) >> 4), keys);
+      umma_commit_w(&bars->s_full[s_turn & 1]);
+      ++s_turn;
+      k_s.next();
       issued_any = true;
       return true;
     };
-    auto issue_dp = [&](const Cursor& c) -> bool {  // dP = dO V^T, once the previous dP has been read
-      if (c.it == 0 && !mbar_wait_w(&bars->do_full, c.item & 1, w, kSiteDo)) return false;
-      if (!mbar_wait_w(&bars->v_full[c.n % C::kVSt], (c.n / C::kVSt) & 1, w, kSiteV)) return false;
-      if (c.n >= 1 && !mbar_wait_w(&bars->dp_free, (c.n - 1) & 1, w, kSiteDpFree)) return false;
+    uint32_t d_turn = 0;  // tiles whose dP has been issued
+    auto issue_dp = [&](int keys) -> bool {  // dP = dO V^T, once the previous dP has been read
+      if (!mbar_wait_w(&bars->v_full[v_d.at], v_d.phase, w, kSiteV)) return false;
+      if (d_turn >= 1 && !mbar_wait_w(&bars->dp_free, (d_turn - 1) & 1, w, kSiteDpFree)) return false;
       tc_fence_after();
-      const uint64_t vd = dV0 + (((c.n % C::kVSt) * C::kTileBytes) >> 4);
-      xt(tmem + kColDP, dDO0, vd, c.width());
+      xt(tmem + kColDP, dDO0, dV0 + ((v_d.at * C::kTileBytes) >> 4), keys);
       umma_commit_w(&bars->dp_full);
-      umma_commit_w(&bars->v_empty[c.n % C::kVSt]);
-      if (c.last()) umma_commit_w(&bars->do_empty);
+      umma_commit_w(&bars->v_empty[v_d.at]);
+      ++d_turn;
+      v_d.next();
       return true;
     };
-    auto issue_dq = [&](const Cursor& c) -> bool {  // dQ += dS K
-      if (!mbar_wait_w(&bars->ds_full, c.n & 1, w, kSiteDs)) return false;
+    auto issue_dq = [&](int keys, bool first) -> bool {  // dQ += dS K
+      if (!mbar_wait_w(&bars->ds_full, q_turn & 1, w, kSiteDs)) return false;
       tc_fence_after();
-      const uint64_t kd = dKmn + (((c.n % C::kKSt) * C::kTileBytes) >> 4);
-      const int steps = c.width() / 16;  // 1, 2 or 8
+      const uint64_t kd = dKmn + ((k_q.at * C::kTileBytes) >> 4);
+      const uint32_t ds = tmem + col_s(q_turn & 1);
       auto step = [&](int kk) {
-        const uint32_t pcol = col_s(c.n & 1) + (kk < 4 ? 0u : 64u) + (kk & 3) * 8;
-        umma_bf16_tmem_a_w(tmem + kColDQ, tmem + pcol, kd + ((kk * 16 * 128) >> 4), kIdKM,
-                           (c.it > 0 || kk > 0) ? 1u : 0u);
+        umma_bf16_tmem_a_w(tmem + kColDQ, ds + (kk < 4 ? 0u : 64u) + (kk & 3) * 8, kd + ((kk * 16 * 128) >> 4), kIdKM,
+                           (!first || kk > 0) ? 1u : 0u);
       };
-      if (steps == kBN / 16) {
+      if (keys == kBN) {
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk) step(kk);
       } else {
 #pragma unroll 1
-        for (int kk = 0; kk < steps; ++kk) step(kk);
+        for (int kk = 0; kk < keys / 16; ++kk) step(kk);
       }
-      umma_commit_w(&bars->dq_done[c.n & 1]);
-      umma_commit_w(&bars->k_empty[c.n % C::kKSt]);
+      umma_commit_w(&bars->dq_done[q_turn & 1]);
+      umma_commit_w(&bars->k_empty[k_q.at]);
+      ++q_turn;
+      k_q.next();
       return true;
     };
     bool ok = true;
-    Cursor c{static_cast<int>(blockIdx.x), 0, 0, 0, DqRun{}};
-    if (c.idx < a.n_items) {
-      c.run = run_of(g, item_of(g, c.idx));
-      Cursor c1 = next(c);
-      ok = issue_s(c) && issue_dp(c);
-      // (S of a second tile only inside the item: the next item's Q shares this one's buffer)
-      bool s1_done = ok && c1.idx < a.n_items && c1.it > 0;
-      if (s1_done) ok = issue_s(c1);
-      while (ok) {
-        const bool more = c1.idx < a.n_items;
-        if (more && c1.it > 0) {
-          // dP of the next tile as soon as this one's has been read, ahead of dQ
-          ok = issue_dp(c1) && issue_dq(c);
-        } else {
-          ok = issue_dq(c);  // the next item's dO may still be on its way
-          if (ok && more) ok = (s1_done || issue_s(c1)) && issue_dp(c1);
-          s1_done = true;
-        }
-        if (!ok || !more) break;
-        const Cursor c2 = next(c1);  // S two tiles ahead
-        s1_done = c2.idx < a.n_items && c2.it > 0;
-        if (s1_done) ok = issue_s(c2);
-        c = c1;
-        c1 = c2;
+    int idx = blockIdx.x;
+    DqRun r{};
+    if (idx < a.n_items) {
+      r = run_of(g, item_of(g, idx));
+      ok = mbar_wait_w(&bars->q_full, 0, w, kSiteQ) && issue_s(r.width(0));
+      if (ok && r.nt == 1) umma_commit_w(&bars->q_empty);
+      ok = ok && mbar_wait_w(&bars->do_full, 0, w, kSiteDo) && issue_dp(r.width(0));
+      if (ok && r.nt == 1) umma_commit_w(&bars->do_empty);
+    }
+    while (ok && idx < a.n_items) {
+      // here the item's first S and dP have been issued
+      const int nt = r.nt, n1 = r.n1, sink = r.kr.n_s, cols = r.kr.cols;
+      auto width = [&](int it) { return sink && (it == 0 || it == n1) ? cols : kBN; };
+      if (nt > 1) {
+        ok = issue_s(width(1));
+        if (nt == 2) umma_commit_w(&bars->q_empty);
       }
+      for (int it = 0; ok && it < nt; ++it) {
+        // dP of the next tile as soon as this one's has been read, ahead of dQ
+        if (it + 1 < nt) {
+          ok = issue_dp(width(it + 1));
+          if (it + 2 == nt) umma_commit_w(&bars->do_empty);
+        }
+        ok = ok && issue_dq(width(it), it == 0);
+        if (ok && it + 2 < nt) {  // S two tiles ahead
+          ok = issue_s(width(it + 2));
+          if (it + 3 == nt) umma_commit_w(&bars->q_empty);
+        }
+      }
+      idx += stride;
+      ++item;
+      if (!ok || idx >= a.n_items) break;
+      // the next item's first tile, behind this one's last dQ: its Q and dO may still be on their way
+      r = run_of(g, item_of(g, idx));
+      ok = mbar_wait_w(&bars->q_full, item & 1, w, kSiteQ) && issue_s(r.width(0));
+      if (ok && r.nt == 1) umma_commit_w(&bars->q_empty);
+      ok = ok && mbar_wait_w(&bars->do_full, item & 1, w, kSiteDo) && issue_dp(r.width(0));
+      if (ok && r.nt == 1) umma_commit_w(&bars->do_empty);
     }
     if (!ok && issued_any) {
       umma_commit_w(&bars->drain);

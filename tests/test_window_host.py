@@ -78,7 +78,11 @@ def decode(**kw):
     (dict(N=0), INVALID), (dict(n=0), INVALID), (dict(cap=0), INVALID), (dict(window=0), INVALID),
     (dict(sinks=-1), INVALID), (dict(D=80), UNSUPPORTED), (dict(Hq=5), UNSUPPORTED), (dict(n=17), UNSUPPORTED),
     (dict(sinks=129), UNSUPPORTED), (dict(ks=(12800, 132, 64)), INVALID), (dict(vs=(-8, 128, 64)), INVALID),
-    (dict(ws=None), WORKSPACE), (dict(nb=0), WORKSPACE), (dict(N=1 << 24, Hq=64), UNSUPPORTED),
+    (dict(N=1 << 24, Hq=64), UNSUPPORTED),
+    # a long cache of one sequence: partials of the splits
+    (dict(N=1, Hkv=1, cap=1 << 20, window=1 << 20, ws=None), WORKSPACE),
+    (dict(N=1, Hkv=1, cap=1 << 20, window=1 << 20, nb=256), WORKSPACE),
+    (dict(N=1, Hkv=1, cap=1 << 20, window=1 << 20, ws=FAKE + 8), WORKSPACE),
 ])
 def test_decode_is_refused(kw, code):
     assert decode(**kw) == code and B_.usp_last_error()
