@@ -19,6 +19,7 @@
 
 #include "usp_attn_common.cuh"
 #include "usp_internal.h"
+#include "usp_ptx.cuh"
 
 namespace usp {
 
@@ -38,50 +39,31 @@ __device__ __forceinline__ int win_lo(const WinGeo& g, int i) {
 }
 
 // Key tiles of the query rows [q0, qe): the sinks of the first row's document
-// below the window tiles, if any, as one tile of up to 128 keys from the
-// document's first on (n_s = 1; a TMA box may start at any row), then the window
-// tiles from w0; nt in all. Few sinks make a narrow tile: the products then take
-// 16 or 32 keys instead of 128.
+// below the window tiles, 32 at a time from the document's first key on (n_s tiles; a
+// TMA box may start at any row), then the window tiles from w0; nt in all. A sink
+// tile's products take 16 or 32 keys instead of 128.
+constexpr int kSinkTile = 32;
 struct KeyRun {
-  int lo, w0, n_s, cols, nt;  // cols: the sink tile's keys in use, rounded up to 16 (128 when more than 32)
-  __device__ __forceinline__ bool sink(int it) const { return it < n_s; }
-  __device__ __forceinline__ int base(int it) const { return it < n_s ? lo : (w0 + it - n_s) * kBN; }
-  // the keys in use of tile it: a multiple of 16
-  __device__ __forceinline__ int width(int it) const { return it < n_s ? cols : kBN; }
+  int lo, w0, n_s, sinks, nt;
+  __device__ __forceinline__ int base(int it) const { return it < n_s ? lo + it * kSinkTile : (w0 + it - n_s) * kBN; }
+  // the keys that the products of tile it take: 16, 32 or 128
+  __device__ __forceinline__ int width(int it) const {
+    return it >= n_s ? kBN : sinks - it * kSinkTile > 16 ? 32 : 16;
+  }
 };
 __device__ __forceinline__ KeyRun key_run(const WinGeo& g, int q0, int qe) {
   KeyRun r;
   r.lo = win_lo(g, q0);
   const int wlo = max(r.lo, q0 - g.W + 1);
   r.w0 = wlo / kBN;
-  const int n = min(r.lo + g.ns, r.w0 * kBN) - r.lo;  // sinks below the window tiles (at most 128)
-  r.n_s = n > 0 ? 1 : 0;
-  r.cols = n > 32 ? kBN : (n + 15) & ~15;
+  r.sinks = max(min(r.lo + g.ns, r.w0 * kBN) - r.lo, 0);  // below the window tiles
+  r.n_s = (r.sinks + kSinkTile - 1) / kSinkTile;
   r.nt = r.n_s + (qe - 1) / kBN + 1 - r.w0;
   return r;
 }
 
-// Visible columns of a tile of KeyRun kr for one query row, 32 from c0 on: the
-// row's window [first, i] and sinks [lo, sink_end) at tile `it`, whose keys start
-// at k0 (a sink tile ends where the window tiles begin).
-struct RowSpan {
-  int lo, first, sink_end, end;  // end: i + 1
-};
-__device__ __forceinline__ RowSpan row_span(const WinGeo& g, int i) {
-  RowSpan r{0, INT_MAX, 0, 0};  // a row past the end of the sequence sees nothing
-  if (i < g.S) {
-    r.lo = win_lo(g, i);
-    r.first = max(r.lo, i - g.W + 1);
-    r.sink_end = min(r.lo + g.ns, i + 1);
-    r.end = i + 1;
-  }
-  return r;
-}
-__device__ __forceinline__ uint32_t bits_between(int a, int b, int c0);
-__device__ __forceinline__ uint32_t visible_bits(const RowSpan& r, const KeyRun& kr, int it, int k0, int c0) {
-  if (kr.sink(it)) return bits_between(r.lo - k0, min(r.sink_end, kr.w0 * kBN) - k0, c0);
-  return bits_between(r.first - k0, r.end - k0, c0) | bits_between(r.lo - k0, r.sink_end - k0, c0);
-}
+// Words of the workspace header behind the status word: the kernels' item counters.
+enum : int { kCounterFwd = 16, kCounterDq = 32, kCounterDkdv = 48 };
 
 // The last query tile in the band of key tile n (its first is n).
 __device__ __forceinline__ int last_qtile(const WinGeo& g, int n) {
@@ -97,6 +79,63 @@ __device__ __forceinline__ uint32_t bits_between(int a, int b, int c0) {
   const uint32_t below_hi = hi >= 32 ? 0xFFFFFFFFu : ((1u << hi) - 1u);
   const uint32_t from_lo = lo >= 32 ? 0u : (0xFFFFFFFFu << lo);
   return below_hi & from_lo;
+}
+
+// ---------------------------------------------------------------- work items
+// Hands a persistent CTA its work items: the first is its block number, each next one
+// the grid's counter says when the CTA is ready for it (items differ: documents, rows
+// walked twice, short walks at the start of a sequence). One warp asks ahead; the
+// others take the number from a slot.
+struct ItemFeed {
+  uint64_t full[2], empty[2];
+  int idx[2];
+};
+__device__ __forceinline__ void feed_init(ItemFeed& f, int takers) {  // takers: warps that call feed_take
+  for (int s = 0; s < 2; ++s) {
+    mbar_init(&f.full[s], 1);
+    mbar_init(&f.empty[s], takers);
+  }
+}
+// The CTA's k-th item (k >= 1), asked for and handed out by the giving warp.
+__device__ __forceinline__ bool feed_give(ItemFeed& f, int k, int* counter, const WaitCtl& w, int site, int& idx) {
+  int x = 0;
+  if ((threadIdx.x & 31) == 0) x = static_cast<int>(gridDim.x) + atomicAdd(counter, 1);
+  idx = __shfl_sync(0xffffffffu, x, 0);
+  const int s = k & 1;
+  if (k > 2 && !mbar_wait_w(&f.empty[s], ((k - 1) / 2 - 1) & 1, w, site)) return false;
+  if ((threadIdx.x & 31) == 0) f.idx[s] = idx;
+  __syncwarp();
+  mbar_arrive_w(&f.full[s]);
+  return true;
+}
+__device__ __forceinline__ bool feed_take(ItemFeed& f, int k, const WaitCtl& w, int site, int& idx) {
+  const int s = k & 1;
+  if (!mbar_wait_w(&f.full[s], ((k - 1) / 2) & 1, w, site)) return false;
+  idx = *reinterpret_cast<volatile int*>(&f.idx[s]);
+  mbar_arrive_warp(&f.empty[s]);
+  return true;
+}
+
+// Programmatic launches: a kernel lets the next one of its stream start once all its
+// CTAs run, and waits for the one before it to end before it touches memory.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <class... P, class... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  if (e == cudaSuccess) note_launch();
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace usp

@@ -62,6 +62,7 @@ struct Bars {
   uint64_t kv_full, kv_empty;
   uint64_t qd_full[2], qd_empty[2];
   uint64_t s_full, dp_full, p_full, ds_full, p_used, ds_used, drain;
+  ItemFeed feed;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -69,6 +70,7 @@ struct Bars {
 enum : int {
   kSiteKvEmpty = 0x501, kSiteQdEmpty = 0x502, kSiteKv = 0x511, kSiteQd = 0x512, kSiteP = 0x513, kSitePUsed = 0x514,
   kSiteDs = 0x515, kSiteDsUsed = 0x516, kSiteS = 0x521, kSiteDp = 0x522, kSiteQdC = 0x523, kSiteEpi = 0x524,
+  kSiteFeed = 0x531,
   kSiteAlign = 0x5FF
 };
 
@@ -107,9 +109,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* sRow = reinterpret_cast<float*>(smem + C::kOffRow);
   const WinGeo& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int stride = gridDim.x;
 
+  let_next_start();
+  wait_for_previous();
   if (threadIdx.x == 0) {
+    feed_init(bars->feed, 1 + kComputeWarps);
     bars->abort_flag = *reinterpret_cast<volatile int*>(a.status) != 0;
     mbar_init(&bars->kv_full, 1);
     mbar_init(&bars->kv_empty, 1);
@@ -147,7 +151,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     int issued = 0, n_kv = 0;
     bool ok = true;
-    for (int idx = blockIdx.x; ok && idx < a.n_items; idx += stride) {
+    int idx = blockIdx.x, next = 0;
+    for (int item = 1; ok && idx < a.n_items; ++item, idx = next) {
       const Item x = item_of(g, idx);
       for (int k = 0; k < x.steps; ++k) {
         const int s = issued % C::kStages;
@@ -176,6 +181,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_4d_w(&tm_v, &bars->kv_full, sV + p * C::kPanelBytes, p * 64, x.gl, x.n * kBN, x.b);
           }
           ++n_kv;
+          if (!feed_give(bars->feed, item, a.status + kCounterDkdv, w, kSiteFeed, next)) {
+            ok = false;
+            break;
+          }
         }
       }
     }
@@ -227,8 +236,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; ok; ++k) {  // k: step of the CTA's stream, it: of the item
         const int s = k % C::kStages, s1 = (k + 1) % C::kStages;
         const bool last = it + 1 == steps;
-        const bool more = !last || idx + stride < a.n_items;
-        const int next_steps = last && more ? item_of(g, idx + stride).steps : steps;
+        if (last && !feed_take(bars->feed, item + 1, w, kSiteFeed, idx)) { ok = false; break; }
+        const bool more = !last || idx < a.n_items;
+        const int next_steps = last && more ? item_of(g, idx).steps : steps;
         if (!mbar_wait_w(&bars->p_full, k & 1, w, kSiteP)) { ok = false; break; }
         tc_fence_after();
         issue_acc(kColDV, kColS, dDOmn, s, it == 0);  // dV += P^T dO
@@ -256,7 +266,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit_w(&bars->dp_full);
         if (last ? next_steps == 1 : it + 2 == steps) umma_commit_w(&bars->kv_empty);
         if (last) {
-          idx += stride;
           steps = next_steps;
           it = 0;
           ++item;
@@ -279,8 +288,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cbase = wg * 64;
     const float2 sl2 = make_float2(g.scale_log2, g.scale_log2);
     bool ok = true;
-    int k = 0;
-    for (int idx = blockIdx.x; ok && idx < a.n_items; idx += stride) {
+    int k = 0, idx = blockIdx.x;
+    for (int item = 1; ok && idx < a.n_items; ++item) {
       const Item x = item_of(g, idx);
       const int k0 = x.n * kBN, j = k0 + row;
       const bool store = j < g.S;
@@ -407,6 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        ok = feed_take(bars->feed, item, w, kSiteFeed, idx);
       }
     }
   }
@@ -441,9 +451,8 @@ cudaError_t launch_d(const WinLaunch& L, cudaStream_t stream) {
   a.n_items = static_cast<int>(items);
   const int sms = sm_count();
   const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);
-  window_dkdv_kernel<D><<<grid, kThreads, C::kSmemBytes, stream>>>(L.tm_q, L.tm_k, L.tm_v, L.tm_do, a);
-  note_launch();
-  return cudaGetLastError();
+  return launch_behind(window_dkdv_kernel<D>, dim3(grid), kThreads, C::kSmemBytes, stream, L.tm_q, L.tm_k, L.tm_v,
+                       L.tm_do, a);
 }
 
 }  // namespace

@@ -12,22 +12,28 @@
 // than 16 query rows, from its own ring of cp.async buffers (no block
 // barrier in the loop) with its own running maximum, sum and O. The streams'
 // results are joined in shared memory; up to 8 splits form a cluster and join
-// through distributed shared memory in the same launch, more write fp32 partials
-// that a second kernel joins by their LSE.
+// through distributed shared memory in the same launch.
+//
+// Few sequences of long and unequal lengths need more: there the CTAs share out the
+// keys of all sequences of a kv head in equal chunks (each works its share out from
+// lens; 4 conversations of 30 to 128 thousand tokens took 199 us in equal splits of
+// each), write fp32 partials, and a second kernel joins a row's by their LSE.
 #include <math.h>
 
 #include "../../include/usp.h"
 #include "usp_internal.h"
 #include "usp_mma.cuh"
 #include "usp_ptx.cuh"
+#include "usp_window.cuh"
 
 namespace usp {
 namespace {
 
 constexpr int kStreams = 4;
 constexpr int kMaxCluster = 8;  // splits that join in one launch (the portable cluster size)
-constexpr int kMaxSplits = 64;
+constexpr int kMaxShares = 296;  // CTAs of a kv head that share out the keys
 constexpr int kSms = 148;
+constexpr float kRescale = 8.f;  // log2 units: O is rescaled only when the maximum grows by more than 2^8
 
 struct DecArgs {
   const __nv_bfloat16 *q, *k, *v;
@@ -35,10 +41,12 @@ struct DecArgs {
   long long k_sn, k_st, k_sh, v_sn, v_st, v_sh;
   __nv_bfloat16* out;
   float* lse;
-  float* o_part;  // [n_splits][N*n*Hq][D] without a cluster
+  // shares: fp32 partials [Hkv][row block][share][row][D] and [..][row]
+  float* o_part;
   float* lse_part;
   int N, n, cap, Hq, Hkv, G, W, ns;
-  int n_splits, cluster;  // cluster: n_splits, or 1 (then more splits write partials)
+  int cluster;   // splits of a sequence that join in the launch
+  int n_shares;  // or, with cluster = 1, the CTAs of a (kv head, row block) that share the keys out; 0: none
   int row_blocks;
   float scale_log2;
 };
@@ -60,6 +68,96 @@ struct DecCfg {
   static_assert(kRows * D * 4 + 3 * kRows * 4 <= kStreamBytes, "results fit over the buffers");
 };
 
+// The keys that any of a sequence's tokens sees, listed: sinks [0, sE), then the window [wlo, len).
+struct SeqKeys {
+  int len, wlo, sE, total;
+};
+__device__ __forceinline__ SeqKeys seq_keys(const DecArgs& a, int seq) {
+  SeqKeys k;
+  k.len = min(max(__ldg(a.lens + seq), 0), a.cap);
+  k.wlo = max(0, k.len - a.n - a.W + 1);
+  k.sE = min(a.ns, k.wlo);
+  k.total = k.sE + k.len - k.wlo;
+  return k;
+}
+
+// How the n_shares CTAs of a kv head share out the keys of all sequences: chunks of `chunk` steps of
+// kStep keys, the smallest that needs no more than n_shares CTAs; ceil(steps / chunk) for a sequence.
+// A warp's work; every lane returns the same.
+template <int kStep>
+struct Shares {
+  int chunk;
+  __device__ __forceinline__ static int steps(const DecArgs& a, int seq) {
+    return (seq_keys(a, seq).total + kStep - 1) / kStep;
+  }
+  __device__ __forceinline__ static int sum(int v) {
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+  }
+  __device__ __forceinline__ int needs(const DecArgs& a, int c) const {
+    const int lane = threadIdx.x & 31;
+    int t = 0;
+    for (int s = lane; s < a.N; s += 32) t += (steps(a, s) + c - 1) / c;
+    return sum(t);
+  }
+  __device__ __forceinline__ void plan(const DecArgs& a) {
+    const int lane = threadIdx.x & 31;
+    long long all = 0;
+    int most = 0;
+    for (int s = lane; s < a.N; s += 32) {
+      const int t = steps(a, s);
+      all += t;
+      most = max(most, t);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) {
+      all += __shfl_xor_sync(0xffffffffu, all, d);
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+    }
+    int lo = static_cast<int>((all + a.n_shares - 1) / a.n_shares), hi = max(most, 1);  // hi: one CTA a sequence
+    lo = max(lo, 1);
+    while (lo < hi) {  // needs() falls with the chunk
+      const int mid = (lo + hi) / 2;
+      if (needs(a, mid) <= a.n_shares)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    chunk = hi;
+  }
+  // The sequence whose share x is, and its number there; false past the last.
+  __device__ __forceinline__ bool locate(const DecArgs& a, int x, int& seq, int& split) const {
+    const int lane = threadIdx.x & 31;
+    int before = 0;
+    for (int s0 = 0; s0 < a.N; s0 += 32) {
+      const int mine = s0 + lane < a.N ? (steps(a, s0 + lane) + chunk - 1) / chunk : 0;
+      int incl = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += v;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, x >= before + incl - mine && x < before + incl);
+      if (hit) {
+        const int who = __ffs(hit) - 1;
+        seq = s0 + who;
+        split = x - before - __shfl_sync(0xffffffffu, incl - mine, who);
+        return true;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return false;
+  }
+  // The first share of sequence seq.
+  __device__ __forceinline__ int first(const DecArgs& a, int seq) const {
+    const int lane = threadIdx.x & 31;
+    int t = 0;
+    for (int s = lane; s < seq; s += 32) t += (steps(a, s) + chunk - 1) / chunk;
+    return sum(t);
+  }
+};
+
 __device__ __forceinline__ float ld_peer(const float* p, int rank) {  // this address in the cluster's CTA `rank`
   uint32_t a;
   float v;
@@ -78,21 +176,33 @@ __global__ void __launch_bounds__(DecCfg<D, kRt>::kThreads, kRt == 1 ? 2 : 1) wi
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g4 = lane >> 2, c4 = lane & 3;
   const int stream = warp & (kStreams - 1), wrt = warp / kStreams;  // the warp's stream and row tile
-  int x = blockIdx.x;
-  const int split = x % a.n_splits;  // a cluster is the splits of one (sequence, kv head, rows)
-  x /= a.n_splits;
-  const int rb = x % a.row_blocks;
-  x /= a.row_blocks;
-  const int kvh = x % a.Hkv, seq = x / a.Hkv;
+  constexpr int kStep = kUnit * kStreams;
+  let_next_start();
+  int x = blockIdx.x, split, seq, rb, kvh, x0, x1, share = 0;
+  if (a.n_shares == 0) {
+    split = x % a.cluster;  // a cluster is the splits of one (sequence, kv head, rows)
+    x /= a.cluster;
+    rb = x % a.row_blocks;
+    x /= a.row_blocks;
+    kvh = x % a.Hkv;
+    seq = x / a.Hkv;
+  } else {
+    share = x;
+    x /= a.n_shares;
+    rb = x % a.row_blocks;
+    kvh = x / a.row_blocks;
+    Shares<kStep> sh;
+    sh.plan(a);
+    if (!sh.locate(a, share % a.n_shares, seq, split)) return;
+    x0 = sh.chunk;
+  }
   const int rows = a.n * a.G;  // rows of a (sequence, kv head): token major, then head of the group
-  const int len = min(max(__ldg(a.lens + seq), 0), a.cap);
-
-  // keys of any of the tokens, listed: sinks [0, sE) and the window [wlo, len)
-  const int wlo = max(0, len - a.n - a.W + 1);
-  const int sE = min(a.ns, wlo);
-  const int total = sE + len - wlo;
-  const int per = ((total + a.n_splits - 1) / a.n_splits + kUnit - 1) / kUnit * kUnit;
-  const int x0 = min(split * per, total), x1 = min(x0 + per, total);
+  const SeqKeys keys = seq_keys(a, seq);
+  const int len = keys.len, wlo = keys.wlo, sE = keys.sE;
+  const long long per = a.n_shares ? static_cast<long long>(x0) * kStep
+                                   : ((keys.total + a.cluster - 1) / a.cluster + kUnit - 1) / kUnit * kUnit;
+  x0 = static_cast<int>(min(split * per, static_cast<long long>(keys.total)));
+  x1 = static_cast<int>(min(x0 + per, static_cast<long long>(keys.total)));
   const int units = (x1 - x0 + kUnit - 1) / kUnit;
   const int mine = units > stream ? (units - stream + kStreams - 1) / kStreams : 0;  // stream, stream + kStreams, ...
 
@@ -166,25 +276,32 @@ __global__ void __launch_bounds__(DecCfg<D, kRt>::kThreads, kRt == 1 ? 2 : 1) wi
       }
     }
     const int base = x0 + (stream + it * kStreams) * kUnit;
+    // a step of window keys that every token sees needs no mask (rows past the last are not written)
+    const int key0 = wlo + base - sE;
+    if (!(base >= sE && base + kUnit <= x1 && key0 + kUnit <= len - a.n + 1 && len - 1 - key0 < a.W)) {
+#pragma unroll
+      for (int u = 0; u < kN; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int xi = base + u * 8 + c4 * 2 + (e & 1), p = pos[e >> 1];
+          const int key = xi < sE ? xi : wlo + xi - sE;
+          if (!(xi < x1 && key <= p && (p - key < a.W || key < a.ns))) sc[u][e] = -INFINITY;
+        }
+    }
     float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int u = 0; u < kN; ++u)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int xi = base + u * 8 + c4 * 2 + (e & 1), p = pos[e >> 1];
-        const int key = xi < sE ? xi : wlo + xi - sE;
-        const bool vis = xi < x1 && key <= p && (p - key < a.W || key < a.ns);
-        sc[u][e] = vis ? sc[u][e] * a.scale_log2 : -INFINITY;
-        mx[e >> 1] = fmaxf(mx[e >> 1], sc[u][e]);
-      }
+      for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], sc[u][e]);
     float alpha[2];
     bool bump = false;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 1));
       mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 2));
+      mx[half] *= a.scale_log2;
       alpha[half] = 1.f;
-      if (mx[half] > m_use[half]) {
+      if (mx[half] > m_use[half] + kRescale) {
         alpha[half] = ex2_approx(m_use[half] - mx[half]);
         m_use[half] = mx[half];
         bump = true;
@@ -203,7 +320,8 @@ __global__ void __launch_bounds__(DecCfg<D, kRt>::kThreads, kRt == 1 ? 2 : 1) wi
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const float ms = m_use[half] == -INFINITY ? 0.f : m_use[half];
-        const float p0 = ex2_approx(sc[u][2 * half] - ms), p1 = ex2_approx(sc[u][2 * half + 1] - ms);
+        const float p0 = ex2_approx(fmaf(sc[u][2 * half], a.scale_log2, -ms));
+        const float p1 = ex2_approx(fmaf(sc[u][2 * half + 1], a.scale_log2, -ms));
         const uint32_t pk = pack_bf16x2(p0, p1);
         rs[half] += p0 + p1;
         const float2 w = add_bf16x2_f32(make_float2(0.f, 0.f), pk);
@@ -320,88 +438,95 @@ __global__ void __launch_bounds__(DecCfg<D, kRt>::kThreads, kRt == 1 ? 2 : 1) wi
   if (!write) return;
   const float inv = lbt > 0.f ? 1.f / lbt : 0.f;
   const float lse = lt > 0.f ? (m + __log2f(lt)) * 0.6931471805599453f : -INFINITY;
+  if (a.n_shares) {
+    const long long prow = static_cast<long long>(share) * C::kRows + r;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e)
+      *reinterpret_cast<float4*>(a.o_part + prow * D + sub * 4 + e * 32) =
+          make_float4(t[e].x * inv, t[e].y * inv, t[e].z * inv, t[e].w * inv);
+    if (sub == 0) a.lse_part[prow] = lse;
+    return;
+  }
   const long long orow =
       (static_cast<long long>(seq) * a.n + gr / a.G) * a.Hq + static_cast<long long>(kvh) * a.G + gr % a.G;
-  const long long n_rows = static_cast<long long>(a.N) * a.n * a.Hq;
-  const bool last = a.n_splits == a.cluster;  // the joined result, not a partial
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) {
-    const int d = sub * 4 + e * 32;
-    if (last) {
-      uint2 pk;
-      pk.x = pack_bf16x2(t[e].x * inv, t[e].y * inv);
-      pk.y = pack_bf16x2(t[e].z * inv, t[e].w * inv);
-      *reinterpret_cast<uint2*>(a.out + orow * D + d) = pk;
-    } else {
-      *reinterpret_cast<float4*>(a.o_part + (split * n_rows + orow) * D + d) =
-          make_float4(t[e].x * inv, t[e].y * inv, t[e].z * inv, t[e].w * inv);
-    }
+    uint2 pk;
+    pk.x = pack_bf16x2(t[e].x * inv, t[e].y * inv);
+    pk.y = pack_bf16x2(t[e].z * inv, t[e].w * inv);
+    *reinterpret_cast<uint2*>(a.out + orow * D + sub * 4 + e * 32) = pk;
   }
-  if (sub == 0) {
-    if (last)
-      a.lse[orow] = lse;
-    else
-      a.lse_part[split * n_rows + orow] = lse;
-  }
+  if (sub == 0) a.lse[orow] = lse;
 }
 
-// The partials' join, a warp per row: its lanes take the splits' LSE, then four columns each, eight
-// splits' loads at a time.
-template <int D>
-__global__ void __launch_bounds__(128) window_join_kernel(const float* __restrict__ o_part,
-                                                          const float* __restrict__ lse_part, int n_splits,
-                                                          long long rows, __nv_bfloat16* __restrict__ out,
-                                                          float* __restrict__ lse) {
-  static_assert(kMaxSplits <= 64, "two splits per lane");
+// The partials' join, a warp per row: its lanes take the shares' LSE, then four columns each, eight
+// shares' loads at a time.
+template <int D, int kRt>
+__global__ void __launch_bounds__(128) window_join_kernel(const DecArgs a) {
+  constexpr int kRows = DecCfg<D, kRt>::kRows, kStep = DecCfg<D, kRt>::kUnit * kStreams;
   const int lane = threadIdx.x & 31;
-  const long long r = (static_cast<long long>(blockIdx.x) * 128 + threadIdx.x) >> 5;
-  if (r >= rows) return;
-  const float l0 = lane < n_splits ? lse_part[lane * rows + r] : -INFINITY;
-  const float l1 = lane + 32 < n_splits ? lse_part[(lane + 32) * rows + r] : -INFINITY;
-  float m = fmaxf(l0, l1);
+  const long long row = (static_cast<long long>(blockIdx.x) * 128 + threadIdx.x) >> 5;  // of [N][n][Hq]
+  if (row >= static_cast<long long>(a.N) * a.n * a.Hq) return;
+  const int h = static_cast<int>(row % a.Hq), t = static_cast<int>(row / a.Hq % a.n);
+  const int seq = static_cast<int>(row / a.Hq / a.n), kvh = h / a.G;
+  const int r = t * a.G + h % a.G;  // row of the (sequence, kv head)
+  Shares<kStep> sh;
+  sh.plan(a);
+  wait_for_previous();  // lens is an input: only the partials are awaited
+  const int n = (Shares<kStep>::steps(a, seq) + sh.chunk - 1) / sh.chunk;
+  const long long first =
+      (static_cast<long long>(kvh) * a.row_blocks + r / kRows) * a.n_shares + sh.first(a, seq);
+  const long long p0 = first * kRows + r % kRows;
+  float m = -INFINITY;
+  for (int s = lane; s < n; s += 32) m = fmaxf(m, a.lse_part[p0 + static_cast<long long>(s) * kRows]);
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
   const float ms = m == -INFINITY ? 0.f : m;
-  const float w0 = expf(l0 - ms), w1 = expf(l1 - ms);
-  float z = w0 + w1;
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) z += __shfl_xor_sync(0xffffffffu, z, d);
   const bool mine = lane * 4 < D;
-  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < n_splits; s0 += 8) {
-    float4 p[8];
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float z = 0.f;
+  for (int s0 = 0; s0 < n; s0 += 32) {
+    const float w = s0 + lane < n ? expf(a.lse_part[p0 + static_cast<long long>(s0 + lane) * kRows] - ms) : 0.f;
+    z += w;
+    const int k = min(32, n - s0);
+    for (int y0 = 0; y0 < k; y0 += 8) {
+      float4 p[8];
 #pragma unroll
-    for (int y = 0; y < 8; ++y)
-      p[y] = mine && s0 + y < n_splits ? *reinterpret_cast<const float4*>(o_part + ((s0 + y) * rows + r) * D + lane * 4)
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int y = 0; y < 8; ++y)
+        p[y] = mine && y0 + y < k
+                   ? *reinterpret_cast<const float4*>(a.o_part + (p0 + static_cast<long long>(s0 + y0 + y) * kRows) * D + lane * 4)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int y = 0; y < 8; ++y) {
-      const float w = __shfl_sync(0xffffffffu, s0 + y < 32 ? w0 : w1, (s0 + y) & 31);
-      t.x += w * p[y].x;
-      t.y += w * p[y].y;
-      t.z += w * p[y].z;
-      t.w += w * p[y].w;
+      for (int y = 0; y < 8; ++y) {
+        const float wy = __shfl_sync(0xffffffffu, w, (y0 + y) & 31);
+        o.x += wy * p[y].x;
+        o.y += wy * p[y].y;
+        o.z += wy * p[y].z;
+        o.w += wy * p[y].w;
+      }
     }
   }
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) z += __shfl_xor_sync(0xffffffffu, z, d);
   const float inv = z > 0.f ? 1.f / z : 0.f;
   if (mine) {
     uint2 pk;
-    pk.x = pack_bf16x2(t.x * inv, t.y * inv);
-    pk.y = pack_bf16x2(t.z * inv, t.w * inv);
-    *reinterpret_cast<uint2*>(out + r * D + lane * 4) = pk;
+    pk.x = pack_bf16x2(o.x * inv, o.y * inv);
+    pk.y = pack_bf16x2(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>(a.out + row * D + lane * 4) = pk;
   }
-  if (lane == 0) lse[r] = z > 0.f ? m + logf(z) : -INFINITY;
+  if (lane == 0) a.lse[row] = z > 0.f ? m + logf(z) : -INFINITY;
 }
 
 struct DecPlan {
-  int rt, row_blocks, n_splits, cluster;
+  int rt, row_blocks, cluster, n_shares;
   size_t ws;
 };
 
-// Splits: as many as fill the SMs (two CTAs each with one row tile a stream, one with two), none
-// shorter than a step per stream. Up to 8 make a cluster of a power of two. More, or a number that
-// is none, pay where rounding down would cost more than the partials' round trip and second launch
-// (about 5 us): from splits of 2048 keys on.
+// Splits of a sequence: as many as fill the SMs (two CTAs each with one row tile a stream, one with
+// two), none shorter than a step per stream, up to 8 in a cluster of a power of two. Where the splits
+// would be longer than 2048 keys (8 us and more) and the SMs hold several CTAs for each sequence, the
+// keys are shared out instead, which costs a second launch (about 5 us) and evens the lengths out.
 DecPlan plan(int N, int n, int cap, int Hq, int Hkv, int D, int window, int sinks) {
   DecPlan p{};
   const int rows = n * (Hq / Hkv);
@@ -409,20 +534,22 @@ DecPlan plan(int N, int n, int cap, int Hq, int Hkv, int D, int window, int sink
   p.row_blocks = (rows + 16 * p.rt - 1) / (16 * p.rt);
   const long long most = static_cast<long long>(window) + n - 1 + sinks;
   const long long keys = most < cap ? most : cap;
-  const long long blocks = static_cast<long long>(N) * Hkv * p.row_blocks;
-  long long s = (p.rt == 1 ? 2LL : 1LL) * kSms / blocks;
+  const long long heads = static_cast<long long>(Hkv) * p.row_blocks;
+  const long long slots = (p.rt == 1 ? 2LL : 1LL) * kSms;
+  long long s = slots / (heads * N);
   const int step = 16 * p.rt * kStreams;
   const long long by_keys = (keys + step - 1) / step;
   if (s > by_keys) s = by_keys;
-  if (s > kMaxSplits) s = kMaxSplits;
   if (s < 1) s = 1;
-  int c = 1;
-  while (2 * c <= s && 2 * c <= kMaxCluster) c *= 2;
   p.cluster = 1;
-  if (c == s || keys / c < 2048) s = p.cluster = c;
-  p.n_splits = static_cast<int>(s);
-  const size_t all = static_cast<size_t>(N) * n * Hq;
-  p.ws = kStatusBytes + (p.n_splits > p.cluster ? p.n_splits * all * (4 * static_cast<size_t>(D) + 4) : 0);
+  while (2 * p.cluster <= s && 2 * p.cluster <= kMaxCluster) p.cluster *= 2;
+  p.ws = kStatusBytes;
+  if (s > 1 && keys / p.cluster >= 2048) {
+    p.cluster = 1;
+    const long long share = slots / heads;
+    p.n_shares = static_cast<int>(share < kMaxShares ? share : kMaxShares);
+    p.ws += static_cast<size_t>(heads) * p.n_shares * (16 * p.rt) * (4 * static_cast<size_t>(D) + 4);
+  }
   return p;
 }
 
@@ -446,15 +573,9 @@ cudaError_t launch_dec(const DecArgs& a, unsigned blocks, cudaStream_t st) {
   e = cudaLaunchKernelEx(&cfg, window_decode_kernel<D, kRt>, a);
   if (e != cudaSuccess) return e;
   note_launch();
-  return cudaGetLastError();
-}
-
-template <int D>
-cudaError_t launch_join(const DecArgs& a, long long rows, cudaStream_t st) {
-  window_join_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(a.o_part, a.lse_part, a.n_splits, rows,
-                                                                            a.out, a.lse);
-  note_launch();
-  return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess || a.n_shares == 0) return e;
+  const long long rows = static_cast<long long>(a.N) * a.n * a.Hq;
+  return launch_behind(window_join_kernel<D, kRt>, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, st, a);
 }
 
 int check(int N, int n, int cap, int Hq, int Hkv, int D, int window, int sinks) {
@@ -467,7 +588,7 @@ int check(int N, int n, int cap, int Hq, int Hkv, int D, int window, int sinks) 
     return record_error(USP_ERR_UNSUPPORTED, "at most %d new tokens a sequence (got %d)", USP_WINDOW_MAX_NEW, n);
   if (sinks > USP_WINDOW_MAX_SINKS)
     return record_error(USP_ERR_UNSUPPORTED, "at most %d sinks (got %d)", USP_WINDOW_MAX_SINKS, sinks);
-  if (static_cast<long long>(N) * n * Hq * kMaxSplits >= (1LL << 31)) return record_error(USP_ERR_UNSUPPORTED, "too many rows");
+  if (static_cast<long long>(N) * n * Hq * 8 >= (1LL << 31)) return record_error(USP_ERR_UNSUPPORTED, "too many rows");
   return USP_OK;
 }
 
@@ -502,7 +623,7 @@ extern "C" int usp_window_attn_decode(const void* q, const void* k_cache, const 
     if (s < 0 || s % 8) return record_error(USP_ERR_INVALID_ARG, "cache strides must be multiples of 8 elements");
   if (window > cap) window = cap;
   const DecPlan p = plan(N, n, cap, Hq, Hkv, D, window, sinks);
-  const bool parts = p.n_splits > p.cluster;
+  const bool parts = p.n_shares > 0;
   if (parts && (!workspace || ws_bytes < p.ws || (reinterpret_cast<uintptr_t>(workspace) & 15u)))
     return record_error(USP_ERR_WORKSPACE, "workspace needs %zu bytes (got %zu)", p.ws, ws_bytes);
   DecArgs a{};
@@ -517,22 +638,20 @@ extern "C" int usp_window_attn_decode(const void* q, const void* k_cache, const 
   a.N = N; a.n = n; a.cap = cap; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv;
   a.W = window;
   a.ns = sinks;
-  a.n_splits = p.n_splits;
   a.cluster = p.cluster;
+  a.n_shares = p.n_shares;
   a.row_blocks = p.row_blocks;
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(D));
-  const long long rows = static_cast<long long>(N) * n * Hq;
+  const long long heads = static_cast<long long>(Hkv) * p.row_blocks;
   if (parts) {
     a.o_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
-    a.lse_part = a.o_part + static_cast<size_t>(p.n_splits) * rows * D;
+    a.lse_part = a.o_part + static_cast<size_t>(heads) * p.n_shares * (16 * p.rt) * D;
   }
-  const long long blocks = static_cast<long long>(N) * Hkv * p.row_blocks * p.n_splits;
+  const long long blocks = parts ? heads * p.n_shares : heads * N * p.cluster;
   if (blocks > 0x7FFFFFFFLL) return record_error(USP_ERR_UNSUPPORTED, "too many rows");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const unsigned nb = static_cast<unsigned>(blocks);
-  cudaError_t e = D == 128 ? (p.rt == 1 ? launch_dec<128, 1>(a, nb, st) : launch_dec<128, 2>(a, nb, st))
-                           : (p.rt == 1 ? launch_dec<64, 1>(a, nb, st) : launch_dec<64, 2>(a, nb, st));
-  if (e == cudaSuccess && parts)
-    e = D == 128 ? launch_join<128>(a, rows, st) : launch_join<64>(a, rows, st);
+  const cudaError_t e = D == 128 ? (p.rt == 1 ? launch_dec<128, 1>(a, nb, st) : launch_dec<128, 2>(a, nb, st))
+                                 : (p.rt == 1 ? launch_dec<64, 1>(a, nb, st) : launch_dec<64, 2>(a, nb, st));
   return e == cudaSuccess ? USP_OK : record_error(USP_ERR_CUDA, "window decode launch: %s", cudaGetErrorString(e));
 }

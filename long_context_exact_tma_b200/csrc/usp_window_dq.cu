@@ -48,7 +48,7 @@ struct Cfg {
   static constexpr int kOffK = 2 * kTileBytes;
   static constexpr int kOffV = kOffK + kKSt * kTileBytes;
   static constexpr int kOffBar = kOffV + kVSt * kTileBytes;
-  static constexpr int kOffRes = kOffBar + 256;  // residues: [item parity][warpgroup][row]
+  static constexpr int kOffRes = kOffBar + 320;  // residues: [item parity][warpgroup][row]
   static constexpr int kSmemBytes = kOffRes + 2 * 2 * 128 * 4;
 };
 
@@ -68,6 +68,7 @@ struct Bars {
   uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
   uint64_t s_full[2], dp_full, dp_free, ds_full, dq_done[2], drain;
   uint64_t r_full;  // both warpgroups' residues of the item are in sRes
+  ItemFeed feed;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -75,7 +76,7 @@ struct Bars {
 enum : int {
   kSiteQEmpty = 0x601, kSiteDoEmpty = 0x602, kSiteKEmpty = 0x603, kSiteVEmpty = 0x604, kSiteQ = 0x611, kSiteDo = 0x612,
   kSiteK = 0x613, kSiteV = 0x614, kSiteDpFree = 0x615, kSiteDs = 0x616, kSiteDqDone = 0x617, kSiteS = 0x621,
-  kSiteDp = 0x622, kSiteEpi = 0x623, kSiteRes = 0x624, kSiteAlign = 0x6FF
+  kSiteDp = 0x622, kSiteEpi = 0x623, kSiteRes = 0x624, kSiteFeed = 0x631, kSiteAlign = 0x6FF
 };
 
 struct Item {
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kOffBar);
-  static_assert(sizeof(Bars) <= 256, "barrier block");
+  static_assert(sizeof(Bars) <= 320, "barrier block");
   uint8_t* sQ = smem + C::kOffQ;
   uint8_t* sDO = smem + C::kOffDO;
   uint8_t* sK = smem + C::kOffK;
@@ -140,9 +141,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* sRes = reinterpret_cast<float*>(smem + C::kOffRes);
   const WinGeo& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int stride = gridDim.x;
 
+  let_next_start();
+  wait_for_previous();
   if (threadIdx.x == 0) {
+    feed_init(bars->feed, 1 + kComputeWarps);
     bars->abort_flag = *reinterpret_cast<volatile int*>(a.status) != 0;
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
@@ -190,7 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_expect_tx_w(bar, C::kTileBytes);
       for (int p = 0; p < C::kPanels; ++p) tma_load_4d_w(tm, bar, dst + p * C::kPanelBytes, p * 64, head, row, b);
     };
-    for (int idx = blockIdx.x; ok && idx < a.n_items; idx += stride) {
+    int idx = blockIdx.x, next = 0;
+    for (int k = 1; ok && idx < a.n_items; ++k, idx = next) {
       const Item x = item_of(g, idx);
       const DqRun kr = run_of(g, x);
       const int kvh = x.h / g.G;
@@ -206,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (n_do >= 1 && !mbar_wait_w(&bars->do_empty, (n_do - 1) & 1, w, kSiteDoEmpty)) { ok = false; break; }
           panels(&tm_do, &bars->do_full, sDO, x.h, x.q0, x.b);
           ++n_do;
+          if (!feed_give(bars->feed, k, a.status + kCounterDq, w, kSiteFeed, next)) { ok = false; break; }
         }
         if (nv >= C::kVSt && !mbar_wait_w(&bars->v_empty[sv], ((nv / C::kVSt) - 1) & 1, w, kSiteVEmpty)) { ok = false; break; }
         panels(&tm_v, &bars->v_full[sv], sV + sv * C::kTileBytes, kvh, kr.base(it), x.b);
@@ -307,8 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     while (ok && idx < a.n_items) {
       // here the item's first S and dP have been issued
-      const int nt = r.nt, n1 = r.n1, sink = r.kr.n_s, cols = r.kr.cols;
-      auto width = [&](int it) { return sink && (it == 0 || it == n1) ? cols : kBN; };
+      const int nt = r.nt;
+      auto width = [&](int it) { return r.width(it); };
       if (nt > 1) {
         ok = issue_s(width(1));
         if (nt == 2) umma_commit_w(&bars->q_empty);
@@ -325,9 +330,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (it + 3 == nt) umma_commit_w(&bars->q_empty);
         }
       }
-      idx += stride;
       ++item;
-      if (!ok || idx >= a.n_items) break;
+      if (!ok || !(ok = feed_take(bars->feed, item, w, kSiteFeed, idx)) || idx >= a.n_items) break;
       // the next item's first tile, behind this one's last dQ: its Q and dO may still be on their way
       r = run_of(g, item_of(g, idx));
       ok = mbar_wait_w(&bars->q_full, item & 1, w, kSiteQ) && issue_s(r.width(0));
@@ -349,8 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cbase = wg * 64;
     const float2 sl2 = make_float2(g.scale_log2, g.scale_log2);
     bool ok = true;
-    int n = 0, item = 0;
-    for (int idx = blockIdx.x; ok && idx < a.n_items; idx += stride, ++item) {
+    int n = 0, item = 0, idx = blockIdx.x;
+    for (; ok && idx < a.n_items; ++item) {
       const Item x = item_of(g, idx);
       const DqRun kr = run_of(g, x);
       const int i = x.q0 + row;
@@ -359,7 +363,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float nl = a.lse2[tab];  // -inf on padding rows: their P is 0
       const float nd = a.delta[tab];
       const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
-      const RowSpan span = row_span(g, i);
+      // visible keys of the row: [first, end) and the sinks [lo, sink_end); none past the end
+      const int lo = store ? win_lo(g, i) : 1 << 30, end = i + 1;
+      const int first = max(lo, i - g.W + 1), sink_end = min(lo + g.ns, i + 1);
+      const int w0 = kr.kr.w0 * kBN;
       const int q_last = min(x.q0 + kBM, g.S) - 1;
       const int first_all = max(win_lo(g, q_last), q_last - g.W + 1);
       float2 res2 = make_float2(0.f, 0.f);
@@ -399,7 +406,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
           reg_fence32(rs);
           if (!whole) {
-            const uint32_t vis = visible_bits(span, kr.kr, kr.pass_it(it), k0, c0);
+            // (a sink tile ends where the window tiles begin)
+            const uint32_t vis = k0 < w0 ? bits_between(lo - k0, min(sink_end, w0) - k0, c0)
+                                         : bits_between(first - k0, end - k0, c0) | bits_between(lo - k0, sink_end - k0, c0);
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (!((vis >> c) & 1u)) {
@@ -459,6 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int q = 0; q < 4; ++q) dst[q] = make_uint4(pk(q * 8), pk(q * 8 + 2), pk(q * 8 + 4), pk(q * 8 + 6));
           }
         }
+        ok = feed_take(bars->feed, item + 1, w, kSiteFeed, idx);
       }
     }
   }
@@ -491,9 +501,7 @@ cudaError_t launch_d(const WinLaunch& L, cudaStream_t stream) {
   a.n_items = static_cast<int>(items);
   const int sms = sm_count();
   const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);
-  window_dq_kernel<D><<<grid, kThreads, C::kSmemBytes, stream>>>(L.tm_q, L.tm_k, L.tm_v, L.tm_do, a);
-  note_launch();
-  return cudaGetLastError();
+  return launch_behind(window_dq_kernel<D>, dim3(grid), kThreads, C::kSmemBytes, stream, L.tm_q, L.tm_k, L.tm_v, L.tm_do, a);
 }
 
 }  // namespace

@@ -13,6 +13,7 @@
 //   warp 1      UMMA issuer: per key tile and query tile t, O_t += P_t V (A = P_t
 //               from TMEM, in two halves of 64 keys), then S_t of the next tile
 //   warps 2..5, 6..9  softmax of tile 0 / 1: thread = query row = TMEM lane
+// The CTAs take the items from a counter as they get ready (ItemFeed).
 // TMEM: S_t / P_t at 128 t, O_t at 256 + 128 t. The key tiles of all items of a
 // CTA form one stream: the S of the next item's first tile is issued behind the
 // last PV of this one, so its loads and products overlap this item's epilogue;
@@ -45,7 +46,7 @@ struct Cfg {
   static constexpr int kOffK = 2 * kTileBytes;
   static constexpr int kOffV = kOffK + kKSt * kTileBytes;
   static constexpr int kOffBar = kOffV + kVSt * kTileBytes;
-  static constexpr int kSmemBytes = kOffBar + 256;
+  static constexpr int kSmemBytes = kOffBar + 320;
 };
 
 struct Args {
@@ -62,13 +63,15 @@ struct Bars {
   uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
   uint64_t s_full[2], p_half[2], p_full[2], pv_done[2];
   uint64_t drain;
+  ItemFeed feed;
   uint32_t tmem_base;
   int abort_flag;
 };
 
 enum : int {
   kSiteQEmpty = 0x401, kSiteKEmpty = 0x402, kSiteVEmpty = 0x403, kSiteQ = 0x411, kSiteK = 0x412, kSiteV = 0x413,
-  kSiteP = 0x414, kSitePvDone = 0x415, kSiteS = 0x421, kSiteO = 0x422, kSiteAlign = 0x4FF
+  kSiteP = 0x414, kSitePvDone = 0x415, kSiteS = 0x421, kSiteO = 0x422,
+  kSiteFeed = 0x431, kSiteAlign = 0x4FF
 };
 
 struct Item {
@@ -111,16 +114,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kOffBar);
-  static_assert(sizeof(Bars) <= 256, "barrier block");
+  static_assert(sizeof(Bars) <= 320, "barrier block");
   uint8_t* sQ = smem + C::kOffQ;
   uint8_t* sK = smem + C::kOffK;
   uint8_t* sV = smem + C::kOffV;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WinGeo& g = a.g;
-  const int stride = gridDim.x;
 
   if (threadIdx.x == 0) {
     bars->abort_flag = *reinterpret_cast<volatile int*>(a.status) != 0;
+    feed_init(bars->feed, 10);  // the V producer, the issuer and eight softmax warps take
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
     for (int s = 0; s < 3; ++s) {
@@ -163,7 +166,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     int issued = 0, n_q = 0;
     bool ok = true;
-    for (int idx = blockIdx.x; ok && idx < a.n_items; idx += stride) {
+    int idx = blockIdx.x, next = 0;
+    for (int k = 1; ok && idx < a.n_items; ++k, idx = next) {
       const Item x = item_of(g, idx);
       const KeyRun kr = key_run(g, x.q0, x.q_end(g));
       for (int it = 0; it < kr.nt; ++it) {
@@ -190,8 +194,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_4d_w(&tm_q, &bars->q_full, sQ + t * C::kTileBytes + p * C::kPanelBytes, p * 64, x.h + t * x.dh,
                             x.q0 + t * x.dq, x.b);
           ++n_q;
+          if (!feed_give(bars->feed, k, a.status + kCounterFwd, w, kSiteFeed, next)) {
+            ok = false;
+            break;
+          }
         }
       }
+      if (ok && !kside) ok = feed_take(bars->feed, k, w, kSiteFeed, next);
     }
     if (*reinterpret_cast<volatile int*>(&bars->abort_flag)) {
       // let every copy this warp started land before the CTA exits
@@ -243,8 +252,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = 0; ok; ++n) {  // n: key tile of the CTA's stream, it: of the item
         const int s = n % C::kVSt, s1 = (n + 1) % C::kKSt;
         const bool last = it + 1 == kr.nt;
-        const bool more = !last || idx + stride < a.n_items;
-        const KeyRun next_kr = last && more ? run_of(idx + stride) : kr;
+        int next = 0;
+        if (last && !feed_take(bars->feed, item + 1, w, kSiteFeed, next)) { ok = false; break; }
+        const bool more = !last || next < a.n_items;
+        const KeyRun next_kr = last && more ? run_of(next) : kr;
         const int next_it = last ? 0 : it + 1;
         const int pv_steps = kr.width(it) / 16;  // 16-key steps of this tile's products: 1, 2 or 8
         if (!mbar_wait_w(&bars->v_full[s], (n / C::kVSt) & 1, w, kSiteV)) { ok = false; break; }
@@ -291,10 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok && more) ok = mbar_wait_w(&bars->q_full, (item + 1) & 1, w, kSiteQ) && next_k() && next_s(0) && next_s(1);
         }
         if (!ok || !more) break;
-        if (last) {
-          idx += stride;
-          ++item;
-        }
+        if (last) ++item;
         kr = next_kr;
         it = next_it;
       }
@@ -313,7 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t cS = col_s(t), cO = col_o(t);
     bool ok = true;
     int n = 0;  // key tile of the CTA's stream
-    for (int idx = blockIdx.x; ok && idx < a.n_items; idx += stride) {
+    int idx = blockIdx.x;
+    for (int k = 1; ok && idx < a.n_items; ++k) {
       const Item x = item_of(g, idx);
       const KeyRun kr = key_run(g, x.q0, x.q_end(g));
       const int h = x.h + t * x.dh, q0 = x.q0 + t * x.dq;
@@ -330,8 +339,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n0 = n;
       const int n_end = n + kr.nt;
       const float2 sl2 = make_float2(g.scale_log2, g.scale_log2);
-      if (kr.n_s && kr.cols <= 32) {
-        // a narrow sink tile, the item's first: one group of 32 columns, no O to rescale yet
+      auto rescale_o = [&](float alpha) {  // the previous PV has landed: S_t is issued behind it
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t o[32];
+          tmem_ld32(trow + cO + c0, o);
+          tmem_ld_wait();
+          reg_fence32(o);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+          tmem_st32(trow + cO + c0, o);
+        }
+      };
+      const int w0 = kr.w0 * kBN;
+      for (int k0 = kr.lo, y = 0; y < kr.n_s; ++y, ++n, k0 += kSinkTile) {  // sink tiles: one group of 32 columns
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[t], n & 1, w, kSiteS));
         if (!ok) break;
         tc_fence_after();
@@ -339,14 +360,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(trow + cS, r);
         tmem_ld_wait();
         reg_fence32(r);
-        const uint32_t vis = bits_between(lo - kr.lo, min(min(lo + g.ns, i + 1), kr.w0 * kBN) - kr.lo, 0);
+        const uint32_t vis = bits_between(lo - k0, min(min(lo + g.ns, i + 1), w0) - k0, 0);
         float mx = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
           if (!((vis >> c) & 1u)) r[c] = 0xFF800000u;
           mx = fmaxf(mx, __uint_as_float(r[c]));
         }
-        m_use = mx * g.scale_log2;
+        const float m_tile = mx * g.scale_log2;
+        const bool bump = m_tile > m_use + (y == 0 ? 0.f : kRescaleThresh);
+        float alpha = 1.f;
+        if (bump) {
+          alpha = ex2_approx(m_use - m_tile);
+          m_use = m_tile;
+        }
+        if (y > 0 && __any_sync(0xffffffffu, bump)) rescale_o(alpha);
         const float m_safe = m_use == -INFINITY ? 0.f : m_use;
         float2 acc = make_float2(0.f, 0.f), accb = acc;
         uint32_t pk[16];
@@ -359,18 +387,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           pk[c >> 1] = pack_bf16x2(pv.x, pv.y);
           accb = add_bf16x2_f32(accb, pk[c >> 1]);
         }
-        l_run = acc.x + acc.y;
-        lb_run = accb.x + accb.y;
+        l_run = l_run * alpha + (acc.x + acc.y);
+        lb_run = lb_run * alpha + (accb.x + accb.y);
         tmem_st16(trow + cS, pk);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive_warp(&bars->p_half[t]);
         mbar_arrive_warp(&bars->p_full[t]);
-        ++n;
       }
-      // keys of the next tile: a wide sink tile's, or the window's first
-      int k0 = kr.n_s && kr.cols > 32 ? kr.lo : kr.w0 * kBN;
-      const int w0 = kr.w0 * kBN;
+      if (!ok) break;
+      int k0 = w0;
       for (; n < n_end; ++n) {
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[t], n & 1, w, kSiteS));
         if (!ok) break;
@@ -386,8 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         reg_fence32(r2);
         reg_fence32(r3);
         if (!(k0 >= first_all && k0 + kBN - 1 <= q0)) {  // not visible as a whole: -inf where it is not
-          const int first = k0 < w0 ? INT_MAX : max(lo, i - g.W + 1);
-          const int sink_end = min(min(lo + g.ns, i + 1), k0 < w0 ? w0 : INT_MAX);
+          const int first = max(lo, i - g.W + 1), sink_end = min(lo + g.ns, i + 1);
           auto hide = [&](uint32_t (&r)[32], int c0) {
             const uint32_t vis = bits_between(first - k0, i + 1 - k0, c0) | bits_between(lo - k0, sink_end - k0, c0);
 #pragma unroll
@@ -439,20 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         emit(r0, 0);
         emit(r1, 16);
-        // the previous PV has landed (S_t is issued behind it): O_t can be rescaled in place
         // before the first half of P is handed over
-        if (n > n0 && __any_sync(0xffffffffu, bump)) {
-#pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            uint32_t o[32];
-            tmem_ld32(trow + cO + c0, o);
-            tmem_ld_wait();
-            reg_fence32(o);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-            tmem_st32(trow + cO + c0, o);
-          }
-        }
+        if (n > n0 && __any_sync(0xffffffffu, bump)) rescale_o(alpha);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive_warp(&bars->p_half[t]);
@@ -465,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive_warp(&bars->p_full[t]);
-        k0 = k0 < w0 ? w0 : k0 + kBN;
+        k0 += kBN;
       }
       // ------------------------------------------------------------ epilogue
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[t], (n - 1) & 1, w, kSiteO));
@@ -493,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (store) a.lse[row_idx] = (m_use + __log2f(l_run)) * 0.6931471805599453f;  // every row sees itself
+        ok = feed_take(bars->feed, k, w, kSiteFeed, idx);
       }
     }
   }

@@ -8,7 +8,7 @@
 #include <math.h>
 
 #include "usp_internal.h"
-#include "usp_ptx.cuh"
+#include "usp_window.cuh"
 
 namespace usp {
 namespace {
@@ -24,6 +24,7 @@ __global__ void __launch_bounds__(kThreads) window_prep_kernel(const uint4* __re
                                                                int Hq, int Lp, long long pad_rows) {
   constexpr int kLanes = D / 8;              // lanes of a row
   constexpr int kRows = 32 / kLanes;         // rows of a step
+  let_next_start();
   const int lane = threadIdx.x & 31;
   const long long warp = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
   const long long r0 = warp * (kRows * kSteps) + lane / kLanes;

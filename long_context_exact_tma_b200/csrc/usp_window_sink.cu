@@ -8,7 +8,9 @@
 //
 // A few keys against every query is bound by reading Q and dO once, so the
 // products run on the warp-level 16x8x16 matrix instruction (a 128-key tensor tile
-// would hold 4 keys in 128): warp = 16 query rows, 16 sinks at a time. A CTA takes
+// would hold 4 keys in 128): warp = 16 query rows, 8 sinks at a time, the sinks
+// always the instruction's 8 columns: S [rows x sinks] and dP with K, V fragments
+// that stay in registers, then dV^T and dK^T [D x sinks]. A CTA takes
 // a run of query tiles of one document and kv head and streams its rows, tile by
 // tile and head by head; every warp fetches its own rows through its own ring of
 // cp.async buffers, so the loop has no block barrier. The warps' fp32 sums are
@@ -25,7 +27,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kGroup = 16;  // sinks at a time
+constexpr int kGroup = 8;   // sinks at a time
 constexpr int kStages = 3;  // (tile, head) steps in flight
 
 struct FarArgs {
@@ -46,9 +48,7 @@ struct FarCfg {
   static constexpr int kHalf = 16 * kRowBytes;
   static constexpr int kStageBytes = 2 * kHalf;  // a warp's 16 rows of Q, then of dO
   static constexpr int kWarpBytes = kStages * kStageBytes;
-  static constexpr int kOffK = kWarps * kWarpBytes;
-  static constexpr int kOffV = kOffK + kGroup * kRowBytes;
-  static constexpr int kOffSum = kOffV + kGroup * kRowBytes;  // fp32 [kGroup][2][D]
+  static constexpr int kOffSum = kWarps * kWarpBytes;  // fp32 [kGroup][2][D]
   static constexpr int kSmemBytes = kOffSum + kGroup * 2 * D * 4;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
@@ -68,6 +68,8 @@ __global__ void __launch_bounds__(kThreads, 1) far_kernel(const FarArgs a) {
   const uint32_t base = smem_addr(smem), mine = base + warp * C::kWarpBytes;
   float* sums = reinterpret_cast<float*>(smem + C::kOffSum);
   const int m_end = min((cx + 1) * a.chunk, g.n_tiles);
+  let_next_start();
+  wait_for_previous();
 
   for (int m0 = cx * a.chunk, m1; m0 < m_end; m0 = m1) {
     // the run [m0, m1): tiles whose first rows are of one document [lo, hi)
@@ -99,31 +101,32 @@ __global__ void __launch_bounds__(kThreads, 1) far_kernel(const FarArgs a) {
       };
       for (int st = 0; st < kStages - 1; ++st) fetch(st);
       __syncthreads();  // the previous group's sums have been written out
-      for (int x = tid; x < kGroup * C::kChunks; x += kThreads) {
-        const int r = x / C::kChunks, ch = x % C::kChunks;
-        uint4 kv = make_uint4(0, 0, 0, 0), vv = kv;
-        if (s0 + r < n_sinks) {
-          const size_t e = ((static_cast<size_t>(b) * g.S + lo + s0 + r) * g.Hkv + gl) * D + ch * 8;
-          kv = *reinterpret_cast<const uint4*>(a.k + e);
-          vv = *reinterpret_cast<const uint4*>(a.v + e);
-        }
-        *reinterpret_cast<uint4*>(smem + C::kOffK + at<D>(r, ch)) = kv;
-        *reinterpret_cast<uint4*>(smem + C::kOffV + at<D>(r, ch)) = vv;
-      }
       for (int x = tid; x < kGroup * 2 * D; x += kThreads) sums[x] = 0.f;
+      // B fragments of K and V: lane (g = lane/4, c = lane%4) holds elements 2c, 2c+1 and 2c+8, 2c+9 of
+      // every 16 of sink g's row
+      uint32_t kb[D / 16][2], vb[D / 16][2];
+      {
+        const int s = s0 + (lane >> 2);
+        const size_t e = ((static_cast<size_t>(b) * g.S + lo + (s < n_sinks ? s : 0)) * g.Hkv + gl) * D + (lane & 3) * 2;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            kb[kk][y] = s < n_sinks ? *reinterpret_cast<const uint32_t*>(a.k + e + kk * 16 + y * 8) : 0u;
+            vb[kk][y] = s < n_sinks ? *reinterpret_cast<const uint32_t*>(a.v + e + kk * 16 + y * 8) : 0u;
+          }
+      }
       __syncthreads();
-      // first far tile of this lane's sink columns (2c, 2c+1 and 2c+8, 2c+9 of the group)
-      int far_from[2][2];
+      // first far tile of this lane's two sink columns
+      int far_from[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int e = 0; e < 2; ++e) {
+        const int s = s0 + (lane & 3) * 2 + e;
+        far_from[e] = s < n_sinks ? last_qtile(g, (lo + s) / kBN) + 1 : INT_MAX;
+      }
+      float av[D / 16][4], ak[D / 16][4];  // dV^T, dK^T: 16 elements x 8 sinks each
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int s = s0 + u * 8 + (lane & 3) * 2 + e;
-          far_from[u][e] = s < n_sinks ? last_qtile(g, (lo + s) / kBN) + 1 : INT_MAX;
-        }
-      float av[D / 8][4], ak[D / 8][4];
-#pragma unroll
-      for (int x = 0; x < D / 8; ++x)
+      for (int x = 0; x < D / 16; ++x)
 #pragma unroll
         for (int e = 0; e < 4; ++e) av[x][e] = ak[x][e] = 0.f;
 
@@ -141,48 +144,41 @@ __global__ void __launch_bounds__(kThreads, 1) far_kernel(const FarArgs a) {
         cp_async_wait<kStages - 1>();
         __syncwarp();
         const uint32_t sq = mine + (st % kStages) * C::kStageBytes, sd = sq + C::kHalf;
-        // S = Q K^T, dP = dO V^T of 16 rows and 16 sinks
+        // S = Q K^T, dP = dO V^T of 16 rows and 8 sinks, even and odd steps apart
         float sc[2][4] = {}, dp[2][4] = {};
-        const int ar = lane & 15, ac = lane >> 4;                              // A rows and half chunks
-        const int br = (lane & 7) + ((lane >> 4) << 3), bc = (lane >> 3) & 1;  // B: sinks and halves
+        const int ar = lane & 15, ac = lane >> 4;  // rows and half chunks of the fragments
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          uint32_t qa[4], da[4], kb[4], vb[4];
+          uint32_t qa[4], da[4];
           ldsm_x4(qa, sq + at<D>(ar, 2 * kk + ac));
           ldsm_x4(da, sd + at<D>(ar, 2 * kk + ac));
-          ldsm_x4(kb, base + C::kOffK + at<D>(br, 2 * kk + bc));
-          ldsm_x4(vb, base + C::kOffV + at<D>(br, 2 * kk + bc));
-          mma_16816(sc[0], qa, kb[0], kb[1]);
-          mma_16816(sc[1], qa, kb[2], kb[3]);
-          mma_16816(dp[0], da, vb[0], vb[1]);
-          mma_16816(dp[1], da, vb[2], vb[3]);
+          mma_16816(sc[kk & 1], qa, kb[kk][0], kb[kk][1]);
+          mma_16816(dp[kk & 1], da, vb[kk][0], vb[kk][1]);
         }
-        uint32_t pt[4], dt[4];  // P^T, dS^T: sinks x rows
+        uint32_t pt[2], dt[2];  // P, dS as B fragments: rows x sinks, rows 0..7 and 8..15
 #pragma unroll
         for (int half = 0; half < 2; ++half) {   // rows i0, i0 + 8
           const bool live = i0 + half * 8 < hi;  // a row of the same document (hi <= S)
+          float p[2], ds[2];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            float p[2], ds[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              p[e] = live && m >= far_from[u][e] ? ex2_approx(sc[u][half * 2 + e] * g.scale_log2 + nl[half]) : 0.f;
-              ds[e] = p[e] * (dp[u][half * 2 + e] + nd[half]);
-            }
-            // bf16 operands, as P and dS have in the key-major kernel; sums stay fp32
-            pt[half * 2 + u] = mov_trans(pack_bf16x2(p[0], p[1]));
-            dt[half * 2 + u] = mov_trans(pack_bf16x2(ds[0], ds[1]));
+          for (int e = 0; e < 2; ++e) {
+            const float sv = sc[0][half * 2 + e] + sc[1][half * 2 + e], dv = dp[0][half * 2 + e] + dp[1][half * 2 + e];
+            p[e] = live && m >= far_from[e] ? ex2_approx(sv * g.scale_log2 + nl[half]) : 0.f;
+            ds[e] = p[e] * (dv + nd[half]);
           }
+          // bf16 operands, as P and dS have in the key-major kernel; sums stay fp32
+          pt[half] = mov_trans(pack_bf16x2(p[0], p[1]));
+          dt[half] = mov_trans(pack_bf16x2(ds[0], ds[1]));
         }
+        // A fragments of dO^T, Q^T: the transposed 8x8 blocks, element octets by row octets
+        const int tr = (lane & 7) + ((lane >> 4) << 3), tc = (lane >> 3) & 1;
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
-          uint32_t db[4], qb[4];
-          ldsm_x4_trans(db, sd + at<D>(ar, 2 * x + ac));
-          ldsm_x4_trans(qb, sq + at<D>(ar, 2 * x + ac));
-          mma_16816(av[2 * x], pt, db[0], db[1]);
-          mma_16816(av[2 * x + 1], pt, db[2], db[3]);
-          mma_16816(ak[2 * x], dt, qb[0], qb[1]);
-          mma_16816(ak[2 * x + 1], dt, qb[2], qb[3]);
+          uint32_t da[4], qa[4];
+          ldsm_x4_trans(da, sd + at<D>(tr, 2 * x + tc));
+          ldsm_x4_trans(qa, sq + at<D>(tr, 2 * x + tc));
+          mma_16816(av[x], da, pt[0], pt[1]);
+          mma_16816(ak[x], qa, dt[0], dt[1]);
         }
         __syncwarp();  // every lane has read the stage before it is filled again
       }
@@ -190,14 +186,12 @@ __global__ void __launch_bounds__(kThreads, 1) far_kernel(const FarArgs a) {
         __syncthreads();
         if (warp == y) {
 #pragma unroll
-          for (int x = 0; x < D / 8; ++x)
+          for (int x = 0; x < D / 16; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-              const int s = (lane >> 2) + (e >> 1) * 8, d = x * 8 + (lane & 3) * 2;
-              float2* tk = reinterpret_cast<float2*>(sums + (s * 2 + 0) * D + d);
-              float2* tv = reinterpret_cast<float2*>(sums + (s * 2 + 1) * D + d);
-              *tk = make_float2(tk->x + ak[x][e], tk->y + ak[x][e + 1]);
-              *tv = make_float2(tv->x + av[x][e], tv->y + av[x][e + 1]);
+            for (int e = 0; e < 4; ++e) {
+              const int s = (lane & 3) * 2 + (e & 1), d = x * 16 + (lane >> 2) + (e >> 1) * 8;
+              sums[(s * 2 + 0) * D + d] += ak[x][e];
+              sums[(s * 2 + 1) * D + d] += av[x][e];
             }
         }
       }
@@ -217,6 +211,8 @@ __global__ void __launch_bounds__(8 * D) far_sum_kernel(const FarArgs a) {
   const WinGeo& g = a.g;
   const int s = blockIdx.x % g.ns, d = blockIdx.x / g.ns % g.n_docs;
   const int gl = blockIdx.x / g.ns / g.n_docs % g.Hkv, b = blockIdx.x / g.ns / g.n_docs / g.Hkv;
+  let_next_start();
+  wait_for_previous();
   int lo = 0, hi = g.S;
   if (g.cu) {
     lo = min(max(__ldg(g.cu + d), 0), g.S);
@@ -258,19 +254,16 @@ cudaError_t launch_d(const WinLaunch& L, cudaStream_t stream) {
   a.part = L.far_part;
   a.sum = L.far_sum;
   const long long heads = static_cast<long long>(L.g.Hkv) * L.g.B;
-  // Longer runs keep the ring of loads full and make fewer partials; a CTA per SM three times
-  // over is worth more.
-  a.chunk = 8;
-  while (a.chunk > 1 && heads * ((L.g.n_tiles + a.chunk - 1) / a.chunk) < 3LL * sm_count()) a.chunk /= 2;
+  // One wave of equal CTAs while the kv heads leave several to each (a run's start and end cost some
+  // microseconds), else three, so that the last wave's idle share is small.
+  const long long sms = sm_count(), per_head = (heads <= sms / 2 ? sms : 3 * sms) / heads;
+  a.chunk = per_head > 1 ? static_cast<int>((L.g.n_tiles + per_head - 1) / per_head) : L.g.n_tiles;
   a.n_chunks = (L.g.n_tiles + a.chunk - 1) / a.chunk;
   const long long n_far = heads * a.n_chunks, n_sum = heads * L.g.n_docs * L.g.ns;
   if (n_far > 0x7FFFFFFFLL || n_sum > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  far_kernel<D><<<static_cast<unsigned>(n_far), kThreads, C::kSmemBytes, stream>>>(a);
-  note_launch();
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  far_sum_kernel<D><<<static_cast<unsigned>(n_sum), 8 * D, 0, stream>>>(a);
-  note_launch();
-  return cudaGetLastError();
+  e = launch_behind(far_kernel<D>, dim3(static_cast<unsigned>(n_far)), kThreads, C::kSmemBytes, stream, a);
+  if (e != cudaSuccess) return e;
+  return launch_behind(far_sum_kernel<D>, dim3(static_cast<unsigned>(n_sum)), 8 * D, 0, stream, a);
 }
 
 }  // namespace

@@ -193,12 +193,17 @@ def decode_ref(q, k, v, lens, W, ns):
     (1, 5, 5000, 24, 3, 128, 5000, 0),
     (2, 1, 9000, 5, 1, 64, 4096, 1),
     (1, 2, 4000, 17, 1, 64, 2048, 3),
+    (1, 1, 20000, 8, 2, 128, 20000, 0),      # keys shared out over the SMs
+    (3, 2, 40001, 10, 1, 128, 33333, 7),     # of unequal sequences, 20 rows a kv head
+    (40, 1, 9000, 3, 1, 64, 9000, 4),        # more sequences than a warp has lanes
 ])
 def test_decode(N, n, cap, Hq, Hkv, D, W, ns, cuda):
     q, k, v = normal(N + cap, N, n, Hq, D), normal(1, N, cap, Hkv, D), normal(2, N, cap, Hkv, D)
     lens = [cap] + [max(0, cap - 1 - 13 * s) for s in range(1, N)]
     if N > 2:
         lens[1], lens[2] = 0, min(n - 1, cap)  # an idle slot; a token before the first
+    if N > 30:
+        lens = [cap - 211 * s if s % 3 else s for s in range(N)]
     k2, v2 = k.clone(), v.clone()
     for s, ln in enumerate(lens):  # what lies past the cached tokens may be anything
         k2[s, ln:], v2[s, ln:] = math.nan, math.inf
