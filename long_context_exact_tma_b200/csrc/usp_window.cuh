@@ -81,6 +81,46 @@ __device__ __forceinline__ uint32_t bits_between(int a, int b, int c0) {
   return below_hi & from_lo;
 }
 
+// ---------------------------------------------------------------- row stores
+// A warp's 32 rows of 32 bf16 columns, row = lane, 64 bytes of it in c: exchanged among
+// groups of four lanes so that lane 4a + k holds 16-byte piece k of rows 4a .. 4a + 3,
+// and a store instruction covers whole 64-byte runs of eight rows. (One row per lane
+// touches 32 cache lines per instruction; an item's stores then cost the CTA 2 us.)
+__device__ __forceinline__ void transpose_pieces(uint4 (&c)[4]) {
+  const int lane = threadIdx.x & 31;
+  auto swap = [&](uint4& keep0, uint4& keep1, int bit) {  // keep0 leaves lanes with the bit set, keep1 the others
+    const bool up = lane & bit;
+    uint4 out = up ? keep0 : keep1;
+    out.x = __shfl_xor_sync(0xffffffffu, out.x, bit);
+    out.y = __shfl_xor_sync(0xffffffffu, out.y, bit);
+    out.z = __shfl_xor_sync(0xffffffffu, out.z, bit);
+    out.w = __shfl_xor_sync(0xffffffffu, out.w, bit);
+    if (up)
+      keep0 = out;
+    else
+      keep1 = out;
+  };
+  swap(c[0], c[1], 1);
+  swap(c[2], c[3], 1);
+  swap(c[0], c[2], 2);
+  swap(c[1], c[3], 2);
+}
+// Row `row0 + lane` of the warp's 32 rows holds 32 columns from c0 on in pk (bf16 pairs); rows below
+// `rows` are stored at base + row * row_step.
+__device__ __forceinline__ void store_rows32(__nv_bfloat16* base, size_t row_step, int row0, int rows, int c0,
+                                             const uint32_t (&pk)[16]) {
+  uint4 c[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) c[q] = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+  transpose_pieces(c);
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = row0 + (lane & ~3) + j;
+    if (r < rows) *reinterpret_cast<uint4*>(base + r * row_step + c0 + (lane & 3) * 8) = c[j];
+  }
+}
+
 // ---------------------------------------------------------------- work items
 // Hands a persistent CTA its work items: the first is its block number, each next one
 // the grid's counter says when the CTA is ready for it (items differ: documents, rows

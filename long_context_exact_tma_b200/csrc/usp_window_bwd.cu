@@ -377,43 +377,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->ds_used, (k - 1) & 1, w, kSiteEpi));
       if (ok) {
         tc_fence_after();
-        const size_t kr = ((static_cast<size_t>(x.b) * g.S + (store ? j : 0)) * g.Hkv + x.gl) * D;
+        const size_t kv0 = (static_cast<size_t>(x.b) * g.S * g.Hkv + x.gl) * D;  // row 0 of the kv head
         const float* far = nullptr;  // the far queries' sums of this key, dK then dV
         if (sink >= 0 && a.far_sum) {
           const int d = g.cu ? doc_of(g.cu, g.n_docs, j) : 0;
           far = a.far_sum +
                 (((static_cast<size_t>(x.b) * g.Hkv + x.gl) * g.n_docs + d) * g.ns + sink) * (2 * D);
         }
-#pragma unroll
-        for (int c0 = wg * (D / 2); c0 < (wg + 1) * (D / 2); c0 += 32) {
-          uint32_t rk[32], rv[32];
-          tmem_ld32(trow + kColDK + c0, rk);
-          tmem_ld32(trow + kColDV + c0, rv);
-          tmem_ld_wait();
-          reg_fence32(rk);
-          reg_fence32(rv);
-          if (store) {
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {  // dK, then dV
+          const uint32_t col = half == 0 ? kColDK : kColDV;
+          const float f = half == 0 ? g.scale : 1.0f;
+          __nv_bfloat16* const dst = (half == 0 ? a.dk : a.dv) + kv0;
+#pragma unroll 1
+          for (int c0 = wg * (D / 2); c0 < (wg + 1) * (D / 2); c0 += 32) {
+            uint32_t r[32], pk[16];
+            tmem_ld32(trow + col + c0, r);
+            tmem_ld_wait();
+            reg_fence32(r);
             if (far) {
 #pragma unroll
-              for (int c = 0; c < 32; ++c) {
-                rk[c] = __float_as_uint(__uint_as_float(rk[c]) + far[c0 + c]);
-                rv[c] = __float_as_uint(__uint_as_float(rv[c]) + far[D + c0 + c]);
-              }
+              for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) + far[half * D + c0 + c]);
             }
-            uint4* dkp = reinterpret_cast<uint4*>(a.dk + kr + c0);
-            uint4* dvp = reinterpret_cast<uint4*>(a.dv + kr + c0);
+            __syncwarp();
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint4 hk, hv;
-              auto pk = [&](int c) {
-                return pack_bf16x2(__uint_as_float(rk[c]) * g.scale, __uint_as_float(rk[c + 1]) * g.scale);
-              };
-              auto pv = [&](int c) { return pack_bf16x2(__uint_as_float(rv[c]), __uint_as_float(rv[c + 1])); };
-              hk = make_uint4(pk(8 * q), pk(8 * q + 2), pk(8 * q + 4), pk(8 * q + 6));
-              hv = make_uint4(pv(8 * q), pv(8 * q + 2), pv(8 * q + 4), pv(8 * q + 6));
-              dkp[q] = hk;
-              dvp[q] = hv;
-            }
+            for (int c = 0; c < 32; c += 2)
+              pk[c >> 1] = pack_bf16x2(__uint_as_float(r[c]) * f, __uint_as_float(r[c + 1]) * f);
+            store_rows32(dst, static_cast<size_t>(g.Hkv) * D, k0 + wq * 32, g.S, c0, pk);
           }
         }
         ok = feed_take(bars->feed, item, w, kSiteFeed, idx);

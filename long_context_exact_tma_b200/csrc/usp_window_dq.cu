@@ -452,21 +452,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->dq_done[(n - 1) & 1], ((n - 1) >> 1) & 1, w, kSiteEpi));
       if (ok) {
         tc_fence_after();
-        const size_t qr = (static_cast<size_t>(x.b) * g.S + (store ? i : 0)) * g.Hq + x.h;
-#pragma unroll
+        __nv_bfloat16* const dq0 = a.dq + (static_cast<size_t>(x.b) * g.S * g.Hq + x.h) * D;  // row 0 of the head
+#pragma unroll 1
         for (int c0 = wg * (D / 2); c0 < (wg + 1) * (D / 2); c0 += 32) {
-          uint32_t o[32];
+          uint32_t o[32], pk[16];
           tmem_ld32(trow + kColDQ + c0, o);
           tmem_ld_wait();
           reg_fence32(o);
-          if (store) {
-            uint4* dst = reinterpret_cast<uint4*>(a.dq + qr * D + c0);
-            auto pk = [&](int c) {
-              return pack_bf16x2(__uint_as_float(o[c]) * g.scale, __uint_as_float(o[c + 1]) * g.scale);
-            };
 #pragma unroll
-            for (int q = 0; q < 4; ++q) dst[q] = make_uint4(pk(q * 8), pk(q * 8 + 2), pk(q * 8 + 4), pk(q * 8 + 6));
-          }
+          for (int c = 0; c < 32; c += 2)
+            pk[c >> 1] = pack_bf16x2(__uint_as_float(o[c]) * g.scale, __uint_as_float(o[c + 1]) * g.scale);
+          store_rows32(dq0, static_cast<size_t>(g.Hq) * D, x.q0 + wq * 32, g.S, c0, pk);
         }
         ok = feed_take(bars->feed, item + 1, w, kSiteFeed, idx);
       }

@@ -486,24 +486,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const float inv_l = lb_run > 0.f ? 1.f / lb_run : 0.f;
         const size_t row_idx = (static_cast<size_t>(x.b) * g.S + (store ? i : 0)) * g.Hq + h;
-#pragma unroll
+        __nv_bfloat16* const o0 = a.out + (static_cast<size_t>(x.b) * g.S * g.Hq + h) * D;  // row 0 of the head
+#pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
-          uint32_t o[32];
+          uint32_t o[32], pk[16];
           tmem_ld32(trow + cO + c0, o);
           tmem_ld_wait();
           reg_fence32(o);
-          if (store) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + row_idx * D + c0);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint4 v;
-              v.x = pack_bf16x2(__uint_as_float(o[q * 8 + 0]) * inv_l, __uint_as_float(o[q * 8 + 1]) * inv_l);
-              v.y = pack_bf16x2(__uint_as_float(o[q * 8 + 2]) * inv_l, __uint_as_float(o[q * 8 + 3]) * inv_l);
-              v.z = pack_bf16x2(__uint_as_float(o[q * 8 + 4]) * inv_l, __uint_as_float(o[q * 8 + 5]) * inv_l);
-              v.w = pack_bf16x2(__uint_as_float(o[q * 8 + 6]) * inv_l, __uint_as_float(o[q * 8 + 7]) * inv_l);
-              dst[q] = v;
-            }
-          }
+          for (int c = 0; c < 32; c += 2)
+            pk[c >> 1] = pack_bf16x2(__uint_as_float(o[c]) * inv_l, __uint_as_float(o[c + 1]) * inv_l);
+          store_rows32(o0, static_cast<size_t>(g.Hq) * D, q0 + wq * 32, g.S, c0, pk);
         }
         if (store) a.lse[row_idx] = (m_use + __log2f(l_run)) * 0.6931471805599453f;  // every row sees itself
         ok = feed_take(bars->feed, k, w, kSiteFeed, idx);
