@@ -178,4 +178,14 @@ cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t s
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
+// Sets the elements of r whose bit of vis is clear (32 columns of one row per lane), most often for
+// all of a warp's rows alike: a group of columns that every row sees costs a vote.
+__device__ __forceinline__ void hide_columns(uint32_t (&r)[32], uint32_t vis, uint32_t value) {
+  if (__all_sync(0xffffffffu, vis == 0xFFFFFFFFu)) return;
+#pragma unroll
+  for (int c = 0; c < 32; ++c)
+    if (!((vis >> c) & 1u)) r[c] = value;
+}
+constexpr uint32_t kMinusInf = 0xFF800000u;
+
 }  // namespace usp

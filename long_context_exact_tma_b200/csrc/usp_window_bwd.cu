@@ -326,10 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
           reg_fence32(rs);
           if (!whole) {
-            const uint32_t vis = bits_between(j - q0, q_end - q0, c0);
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!((vis >> c) & 1u)) rs[c] = 0xFF800000u;
+            hide_columns(rs, bits_between(j - q0, q_end - q0, c0), kMinusInf);
           }
           uint32_t pk[16];
 #pragma unroll

@@ -409,12 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (a sink tile ends where the window tiles begin)
             const uint32_t vis = k0 < w0 ? bits_between(lo - k0, min(sink_end, w0) - k0, c0)
                                          : bits_between(first - k0, end - k0, c0) | bits_between(lo - k0, sink_end - k0, c0);
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!((vis >> c) & 1u)) {
-                rs[c] = 0xFF800000u;
-                rp[half][c] = 0u;  // columns past a narrow tile's width hold what an earlier tile left
-              }
+            hide_columns(rs, vis, kMinusInf);
+            hide_columns(rp[half], vis, 0u);  // columns past a narrow tile's width hold what an earlier tile left
           }
           uint32_t dk[16];
           if (it < kr.n1) {

@@ -414,10 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(k0 >= first_all && k0 + kBN - 1 <= q0)) {  // not visible as a whole: -inf where it is not
           const int first = max(lo, i - g.W + 1), sink_end = min(lo + g.ns, i + 1);
           auto hide = [&](uint32_t (&r)[32], int c0) {
-            const uint32_t vis = bits_between(first - k0, i + 1 - k0, c0) | bits_between(lo - k0, sink_end - k0, c0);
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!((vis >> c) & 1u)) r[c] = 0xFF800000u;
+            hide_columns(r, bits_between(first - k0, i + 1 - k0, c0) | bits_between(lo - k0, sink_end - k0, c0), kMinusInf);
           };
           hide(r0, 0);
           hide(r1, 32);

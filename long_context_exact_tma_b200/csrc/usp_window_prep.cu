@@ -54,8 +54,10 @@ __global__ void __launch_bounds__(kThreads) window_prep_kernel(const uint4* __re
     for (int o = kLanes / 2; o > 0; o /= 2) t += __shfl_xor_sync(0xffffffffu, t, o);
     const long long r = r0 + s * kRows;
     if (lane % kLanes == 0 && r < rows) {
-      const long long h = r % Hq, bs = r / Hq;
-      const long long dst = ((bs / S) * Hq + h) * Lp + bs % S;
+      // (rows have 31-bit numbers: 64-bit divisions made this kernel's time, 67 us for 524288 rows)
+      const uint32_t r32 = static_cast<uint32_t>(r), bs = r32 / static_cast<uint32_t>(Hq), h = r32 - bs * Hq;
+      const uint32_t bi = bs / static_cast<uint32_t>(S), row = bs - bi * S;
+      const size_t dst = (static_cast<size_t>(bi) * Hq + h) * Lp + row;
       const float l = lse[r];
       delta_t[dst] = -t;
       lse2_t[dst] = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
