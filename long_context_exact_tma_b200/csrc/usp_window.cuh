@@ -81,6 +81,19 @@ __device__ __forceinline__ uint32_t bits_between(int a, int b, int c0) {
   return below_hi & from_lo;
 }
 
+// A position in a ring of kN stages: the stage, and the parity of its current use.
+template <int kN>
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == kN) {
+      at = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
 // ---------------------------------------------------------------- row stores
 // A warp's 32 rows of 32 bf16 columns, row = lane, 64 bytes of it in c: exchanged among
 // groups of four lanes so that lane 4a + k holds 16-byte piece k of rows 4a .. 4a + 3,

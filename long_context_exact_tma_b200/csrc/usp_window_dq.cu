@@ -108,19 +108,6 @@ __device__ __forceinline__ DqRun run_of(const WinGeo& g, const Item& x) {
   return r;
 }
 
-// A position in a ring of kN stages: the stage, and the parity of its current use.
-template <int kN>
-struct Ring {
-  int at = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next() {
-    if (++at == kN) {
-      at = 0;
-      phase ^= 1u;
-    }
-  }
-};
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,

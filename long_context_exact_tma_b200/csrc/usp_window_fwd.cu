@@ -7,7 +7,7 @@
 // A persistent CTA (one per SM, 352 threads) takes work items: two 128-row query
 // tiles that share every key tile -- the same rows of two heads of a group when
 // the group is even (then both tiles need exactly the same keys), else two
-// consecutive row tiles of a head. Roles:
+// consecutive row tiles of a head, each taking the key tiles of its own window. Roles:
 //   warp 0      TMA producer of K (3 stages) and of the item's two Q tiles
 //   warp 10     TMA producer of V
 //   warp 1      UMMA issuer: per key tile and query tile t, O_t += P_t V (A = P_t
@@ -103,7 +103,38 @@ __device__ __forceinline__ Item item_of(const WinGeo& g, int idx) {
   return x;
 }
 
-template <int D>
+// The key tiles of an item, and those of them that query tile t takes: the sinks' and
+// the window's [begin[t], end[t]) (numbers of the run); none at all without rows.
+struct ItemRun {
+  KeyRun kr;
+  int begin1, end0, end1;  // tile 0 begins, and the later of the two ends, with the run
+  __device__ __forceinline__ bool takes(int t, int it) const {
+    return t == 0 ? it < end0 : it < end1 && (it < kr.n_s || it >= begin1);
+  }
+};
+__device__ __forceinline__ ItemRun run_of(const WinGeo& g, const Item& x) {
+  ItemRun r;
+  r.kr = key_run(g, x.q0, x.q_end(g));
+  r.end0 = r.end1 = r.kr.nt;
+  r.begin1 = r.kr.n_s;
+  if (x.dq) {
+    const int q1 = x.q0 + x.dq;
+    if (q1 < g.S) {
+      const int lo1 = win_lo(g, q1);
+      r.end0 = r.kr.nt - 1;
+      int first = max(lo1, q1 - g.W + 1) / kBN;
+      // its sinks may lie among the window's first tiles
+      if (lo1 + g.ns > r.kr.w0 * kBN) first = min(first, lo1 / kBN);
+      r.begin1 = r.kr.n_s + max(first - r.kr.w0, 0);
+    } else {
+      r.end1 = 0;
+    }
+  }
+  return r;
+}
+
+// kHeads: the items' tiles are two heads of a group (both take every key tile).
+template <int D, bool kHeads>
 __global__ void __launch_bounds__(kThreads, 1)
     window_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const Args a) {
@@ -215,97 +246,96 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dQ0 = sdesc_sw128(smem_addr(sQ), 16, 1024);
     const uint64_t dK0 = sdesc_sw128(smem_addr(sK), 16, 1024);
     const uint64_t dV0 = sdesc_sw128(smem_addr(sV), C::kPanelBytes, 1024);
-    // S_t = Q_t K^T with stage ks; the narrow form takes the stage's first `keys` (16 or 32)
-    auto issue_s_as = [&](int t, int ks, uint32_t idesc) {
-      const uint64_t qd = dQ0 + ((t * C::kTileBytes) >> 4), kd = dK0 + ((ks * C::kTileBytes) >> 4);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = ((kk >> 2) * C::kPanelBytes + (kk & 3) * 32) >> 4;
-        umma_bf16_w(tmem + col_s(t), qd + off, kd + off, idesc, kk > 0 ? 1u : 0u);
-      }
-      umma_commit_w(&bars->s_full[t]);
-    };
-    auto issue_s = [&](int t, int ks, int keys) {
-      if (keys == kBN)
-        issue_s_as(t, ks, idesc_bf16_f32(kBM, kBN, 0, 0));
-      else
-        issue_s_as(t, ks, idesc_bf16_f32(kBM, keys, 0, 0));
-    };
-    auto run_of = [&](int idx) {
-      const Item x = item_of(g, idx);
-      return key_run(g, x.q0, x.q_end(g));
-    };
     bool ok = true, issued_any = false;
-    int idx = blockIdx.x;
-    if (idx < a.n_items) {
-      KeyRun kr = run_of(idx);
-      int it = 0, item = 0;
-      ok = mbar_wait_w(&bars->q_full, 0, w, kSiteQ) && mbar_wait_w(&bars->k_full[0], 0, w, kSiteK);
-      if (ok) {
-        tc_fence_after();
-        issue_s(0, 0, kr.width(0));
-        issue_s(1, 0, kr.width(0));
-        umma_commit_w(&bars->k_empty[0]);
-        if (kr.nt == 1) umma_commit_w(&bars->q_empty);
-        issued_any = true;
-      }
-      for (int n = 0; ok; ++n) {  // n: key tile of the CTA's stream, it: of the item
-        const int s = n % C::kVSt, s1 = (n + 1) % C::kKSt;
-        const bool last = it + 1 == kr.nt;
-        int next = 0;
-        if (last && !feed_take(bars->feed, item + 1, w, kSiteFeed, next)) { ok = false; break; }
-        const bool more = !last || next < a.n_items;
-        const KeyRun next_kr = last && more ? run_of(next) : kr;
-        const int next_it = last ? 0 : it + 1;
-        const int pv_steps = kr.width(it) / 16;  // 16-key steps of this tile's products: 1, 2 or 8
-        if (!mbar_wait_w(&bars->v_full[s], (n / C::kVSt) & 1, w, kSiteV)) { ok = false; break; }
-        const uint64_t vd = dV0 + ((s * C::kTileBytes) >> 4);
-        auto issue_pv = [&](int t) -> bool {  // in two halves of 64 keys, each as soon as its P is in TMEM
-          if (!mbar_wait_w(&bars->p_half[t], n & 1, w, kSiteP)) return false;
-          tc_fence_after();
-          if (pv_steps == kBN / 16) {
+    Ring<C::kKSt> k_s;                // the K stage that S takes next
+    Ring<C::kVSt> v_p;                // the V stage that PV takes
+    uint32_t n_pv[2] = {0, 0};        // PV issued so far of each query tile
+    // S_t = Q_t K^T with the first `keys` rows of stage k_s (128; 16 or 32 in a sink tile); it overwrites
+    // P_t, so it waits for the last PV_t
+    auto issue_s = [&](int t, int keys) -> bool {
+      if (n_pv[t] > 0 && !mbar_wait_w(&bars->pv_done[t], (n_pv[t] - 1) & 1, w, kSitePvDone)) return false;
+      tc_fence_after();
+      const uint64_t qd = dQ0 + ((t * C::kTileBytes) >> 4), kd = dK0 + ((k_s.at * C::kTileBytes) >> 4);
+      auto go = [&](uint32_t idesc) {
 #pragma unroll
-            for (int kk = 0; kk < kBN / 32; ++kk)
-              umma_bf16_tmem_a_w(tmem + col_o(t), tmem + col_s(t) + kk * 8, vd + ((kk * 16 * 128) >> 4), kIdescPV,
-                                 (it > 0 || kk > 0) ? 1u : 0u);
-            if (!mbar_wait_w(&bars->p_full[t], n & 1, w, kSiteP)) return false;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = kBN / 32; kk < kBN / 16; ++kk)
-              umma_bf16_tmem_a_w(tmem + col_o(t), tmem + col_s(t) + kk * 8, vd + ((kk * 16 * 128) >> 4), kIdescPV, 1u);
-          } else {  // a narrow tile: one or two steps, all of its P handed over at once
-#pragma unroll 1
-            for (int kk = 0; kk < pv_steps; ++kk)
-              umma_bf16_tmem_a_w(tmem + col_o(t), tmem + col_s(t) + kk * 8, vd + ((kk * 16 * 128) >> 4), kIdescPV,
-                                 (it > 0 || kk > 0) ? 1u : 0u);
-            if (!mbar_wait_w(&bars->p_full[t], n & 1, w, kSiteP)) return false;
-          }
-          umma_commit_w(&bars->pv_done[t]);
-          if (t == 1) umma_commit_w(&bars->v_empty[s]);
-          return true;
-        };
-        auto next_s = [&](int t) -> bool {  // S_t of the next tile overwrites P_t: behind this tile's PV_t
-          if (!mbar_wait_w(&bars->pv_done[t], n & 1, w, kSitePvDone)) return false;
-          tc_fence_after();
-          issue_s(t, s1, next_kr.width(next_it));
-          if (t == 1) {
-            umma_commit_w(&bars->k_empty[s1]);
-            if (next_it + 1 == next_kr.nt) umma_commit_w(&bars->q_empty);
-          }
-          return true;
-        };
-        auto next_k = [&]() { return mbar_wait_w(&bars->k_full[s1], ((n + 1) / C::kKSt) & 1, w, kSiteK); };
-        if (!last) {
-          ok = issue_pv(0) && next_k() && next_s(0) && issue_pv(1) && next_s(1);
-        } else {  // the next item's Q may still be on its way: this item's products first
-          ok = issue_pv(0) && issue_pv(1);
-          if (ok && more) ok = mbar_wait_w(&bars->q_full, (item + 1) & 1, w, kSiteQ) && next_k() && next_s(0) && next_s(1);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * C::kPanelBytes + (kk & 3) * 32) >> 4;
+          umma_bf16_w(tmem + col_s(t), qd + off, kd + off, idesc, kk > 0 ? 1u : 0u);
         }
-        if (!ok || !more) break;
-        if (last) ++item;
-        kr = next_kr;
-        it = next_it;
+      };
+      if (keys == kBN)
+        go(idesc_bf16_f32(kBM, kBN, 0, 0));
+      else
+        go(idesc_bf16_f32(kBM, keys, 0, 0));
+      umma_commit_w(&bars->s_full[t]);
+      issued_any = true;
+      return true;
+    };
+    // O_t += P_t V in two halves of 64 keys, each as soon as its P is in TMEM
+    auto issue_pv = [&](int t, int keys, bool first) -> bool {
+      if (!mbar_wait_w(&bars->p_half[t], n_pv[t] & 1, w, kSiteP)) return false;
+      tc_fence_after();
+      const uint64_t vd = dV0 + ((v_p.at * C::kTileBytes) >> 4);
+      auto step = [&](int kk) {
+        umma_bf16_tmem_a_w(tmem + col_o(t), tmem + col_s(t) + kk * 8, vd + ((kk * 16 * 128) >> 4), kIdescPV,
+                           (!first || kk > 0) ? 1u : 0u);
+      };
+      if (keys == kBN) {
+#pragma unroll
+        for (int kk = 0; kk < kBN / 32; ++kk) step(kk);
+        if (!mbar_wait_w(&bars->p_full[t], n_pv[t] & 1, w, kSiteP)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = kBN / 32; kk < kBN / 16; ++kk) step(kk);
+      } else {  // a sink tile: one or two steps, all of its P handed over at once
+#pragma unroll 1
+        for (int kk = 0; kk < keys / 16; ++kk) step(kk);
+        if (!mbar_wait_w(&bars->p_full[t], n_pv[t] & 1, w, kSiteP)) return false;
       }
+      umma_commit_w(&bars->pv_done[t]);
+      ++n_pv[t];
+      return true;
+    };
+    uint32_t item = 0;
+    int idx = blockIdx.x;
+    while (ok && idx < a.n_items) {
+      const ItemRun r = run_of(g, item_of(g, idx));
+      const int nt = r.kr.nt;
+      // the item's first S, behind the last PV of the item before
+      ok = mbar_wait_w(&bars->q_full, item & 1, w, kSiteQ) && mbar_wait_w(&bars->k_full[k_s.at], k_s.phase, w, kSiteK);
+      for (int t = 0; ok && t < 2; ++t)
+        if (kHeads || r.takes(t, 0)) ok = issue_s(t, r.kr.width(0));
+      if (!ok) break;
+      umma_commit_w(&bars->k_empty[k_s.at]);
+      k_s.next();
+      if (nt == 1) umma_commit_w(&bars->q_empty);
+      for (int it = 0; ok && it < nt; ++it) {
+        if (!mbar_wait_w(&bars->v_full[v_p.at], v_p.phase, w, kSiteV)) { ok = false; break; }
+        const bool more = it + 1 < nt;
+        // per query tile PV_t, then S_t of the next key tile: the tensor core runs one tile's products
+        // while the other's softmax works
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if ((kHeads || r.takes(t, it)) && !issue_pv(t, r.kr.width(it), kHeads || t == 0 || r.kr.n_s > 0 ? it == 0 : it == r.begin1)) {
+            ok = false;
+            break;
+          }
+          if (t == 1) umma_commit_w(&bars->v_empty[v_p.at]);
+          if (more) {
+            if (t == 0 && !mbar_wait_w(&bars->k_full[k_s.at], k_s.phase, w, kSiteK)) { ok = false; break; }
+            if ((kHeads || r.takes(t, it + 1)) && !issue_s(t, r.kr.width(it + 1))) { ok = false; break; }
+            if (t == 1) {
+              umma_commit_w(&bars->k_empty[k_s.at]);
+              if (it + 2 == nt) umma_commit_w(&bars->q_empty);
+            }
+          }
+        }
+        if (!ok) break;
+        v_p.next();
+        if (more) k_s.next();
+      }
+      ++item;
+      if (ok) ok = feed_take(bars->feed, item, w, kSiteFeed, idx);
     }
     if (!ok && issued_any) {
       umma_commit_w(&bars->drain);
@@ -324,7 +354,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int idx = blockIdx.x;
     for (int k = 1; ok && idx < a.n_items; ++k) {
       const Item x = item_of(g, idx);
-      const KeyRun kr = key_run(g, x.q0, x.q_end(g));
+      const ItemRun r = run_of(g, x);
+      const KeyRun& kr = r.kr;
       const int h = x.h + t * x.dh, q0 = x.q0 + t * x.dq;
       const int i = q0 + row;
       const bool store = i < g.S;
@@ -337,7 +368,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // PV product takes (O's divisor, so that O stays a convex combination of V rows)
       float m_use = -INFINITY, l_run = 0.f, lb_run = 0.f;
       const int n0 = n;
-      const int n_end = n + kr.nt;
+      // this tile's window tiles, from k0 on, behind the sinks'
+      const int t_begin = kHeads || t == 0 ? kr.n_s : r.begin1, t_end = kHeads ? kr.nt : t == 0 ? r.end0 : r.end1;
+      const int n_sink = t_end > 0 ? kr.n_s : 0, n_end = n + n_sink + max(t_end - t_begin, 0);
       const float2 sl2 = make_float2(g.scale_log2, g.scale_log2);
       auto rescale_o = [&](float alpha) {  // the previous PV has landed: S_t is issued behind it
 #pragma unroll
@@ -352,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       const int w0 = kr.w0 * kBN;
-      for (int k0 = kr.lo, y = 0; y < kr.n_s; ++y, ++n, k0 += kSinkTile) {  // sink tiles: one group of 32 columns
+      for (int k0 = kr.lo, y = 0; y < n_sink; ++y, ++n, k0 += kSinkTile) {  // sink tiles: one group of 32 columns
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[t], n & 1, w, kSiteS));
         if (!ok) break;
         tc_fence_after();
@@ -396,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_warp(&bars->p_full[t]);
       }
       if (!ok) break;
-      int k0 = w0;
+      int k0 = w0 + (t_begin - kr.n_s) * kBN;
       for (; n < n_end; ++n) {
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[t], n & 1, w, kSiteS));
         if (!ok) break;
@@ -478,8 +511,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         k0 += kBN;
       }
       // ------------------------------------------------------------ epilogue
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[t], (n - 1) & 1, w, kSiteO));
-      if (ok) {
+      if (ok && n > n0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[t], (n - 1) & 1, w, kSiteO));
+      if (ok && n > n0) {
         tc_fence_after();
         const float inv_l = lb_run > 0.f ? 1.f / lb_run : 0.f;
         const size_t row_idx = (static_cast<size_t>(x.b) * g.S + (store ? i : 0)) * g.Hq + h;
@@ -496,8 +529,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           store_rows32(o0, static_cast<size_t>(g.Hq) * D, q0 + wq * 32, g.S, c0, pk);
         }
         if (store) a.lse[row_idx] = (m_use + __log2f(l_run)) * 0.6931471805599453f;  // every row sees itself
-        ok = feed_take(bars->feed, k, w, kSiteFeed, idx);
       }
+      if (ok) ok = feed_take(bars->feed, k, w, kSiteFeed, idx);
     }
   }
 
@@ -509,16 +542,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool kHeads>
 cudaError_t launch_d(const WinLaunch& L, cudaStream_t stream) {
   using C = Cfg<D>;
   static_assert(C::kSmemBytes <= 227 * 1024, "shared memory budget");
   cudaError_t e =
-      cudaFuncSetAttribute(window_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+      cudaFuncSetAttribute(window_fwd_kernel<D, kHeads>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
   Args a{};
   a.g = L.g;
-  a.g.pair_heads = L.g.G % 2 == 0;
+  a.g.pair_heads = kHeads;
   a.out = static_cast<__nv_bfloat16*>(L.out);
   a.lse = L.lse;
   a.status = L.status;
@@ -529,7 +562,7 @@ cudaError_t launch_d(const WinLaunch& L, cudaStream_t stream) {
   a.n_items = static_cast<int>(items);
   const int sms = sm_count();
   const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);
-  window_fwd_kernel<D><<<grid, kThreads, C::kSmemBytes, stream>>>(L.tm_q, L.tm_k, L.tm_v, a);
+  window_fwd_kernel<D, kHeads><<<grid, kThreads, C::kSmemBytes, stream>>>(L.tm_q, L.tm_k, L.tm_v, a);
   note_launch();
   return cudaGetLastError();
 }
@@ -537,7 +570,10 @@ cudaError_t launch_d(const WinLaunch& L, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_window_fwd(const WinLaunch& L, cudaStream_t stream) {
-  return L.D == 128 ? launch_d<128>(L, stream) : L.D == 64 ? launch_d<64>(L, stream) : cudaErrorInvalidValue;
+  const bool heads = L.g.G % 2 == 0;
+  if (L.D == 128) return heads ? launch_d<128, true>(L, stream) : launch_d<128, false>(L, stream);
+  if (L.D == 64) return heads ? launch_d<64, true>(L, stream) : launch_d<64, false>(L, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace usp
