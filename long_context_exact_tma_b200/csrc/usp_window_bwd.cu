@@ -80,10 +80,11 @@ struct Item {
 };
 __device__ __forceinline__ Item item_of(const WinGeo& g, int idx) {
   Item x;
-  x.n = idx % g.n_tiles;
-  idx /= g.n_tiles;
+  // the first keys of every head first (the causally heaviest), the heads side by side
   x.gl = idx % g.Hkv;
-  x.b = idx / g.Hkv;
+  idx /= g.Hkv;
+  x.b = idx % g.B;
+  x.n = idx / g.B;
   x.n_m = last_qtile(g, x.n) - x.n + 1;
   x.steps = x.n_m * g.G;
   return x;

@@ -84,10 +84,11 @@ struct Item {
 };
 __device__ __forceinline__ Item item_of(const WinGeo& g, int idx) {
   Item x;
-  x.q0 = (g.n_tiles - 1 - idx % g.n_tiles) * kBM;  // the causally heaviest first
-  idx /= g.n_tiles;
+  // as in the forward: the last rows of every head first, the heads side by side
   x.h = idx % g.Hq;
-  x.b = idx / g.Hq;
+  idx /= g.Hq;
+  x.b = idx % g.B;
+  x.q0 = (g.n_tiles - 1 - idx / g.B) * kBM;
   return x;
 }
 // The item's key tiles, twice where a row has few keys.

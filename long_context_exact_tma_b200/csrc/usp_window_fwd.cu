@@ -80,15 +80,17 @@ struct Item {
   __device__ __forceinline__ int q_end(const WinGeo& g) const { return min(q0 + dq + kBM, g.S); }
 };
 
-// Items of one head unit run from the last rows back (the causally heaviest first).
+// The last rows of every head come first, the heads of a batch side by side: their
+// key tiles are in L2 for the rows before them, and the short walks of the first rows
+// fill the end of the launch.
 __device__ __forceinline__ Item item_of(const WinGeo& g, int idx) {
   Item x;
   const int n_m = g.pair_heads ? g.n_tiles : (g.n_tiles + 1) / 2;
-  const int m = n_m - 1 - idx % n_m;
-  idx /= n_m;
   const int n_u = g.pair_heads ? g.Hq / 2 : g.Hq;
   const int u = idx % n_u;
-  x.b = idx / n_u;
+  idx /= n_u;
+  x.b = idx % g.B;
+  const int m = n_m - 1 - idx / g.B;
   if (g.pair_heads) {
     x.h = 2 * u;
     x.q0 = m * kBM;
