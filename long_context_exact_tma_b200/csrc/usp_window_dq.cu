@@ -16,7 +16,7 @@
 // r_i sum_j P_ij k_j, which matters next to dQ's own rounding only where few keys
 // share a row's weight (the ratio falls with the root of their number: 1.2 of the
 // rounding at 4 keys, 0.4 at 64): query tiles with rows of fewer than 48 keys walk
-// their key tiles twice, the second time with dS = -r_i P_ij.
+// the tiles of those rows' keys twice, the second time with dS = -r_i P_ij.
 //
 // TMEM: S / dS at 0 and 128, dP at 256, dQ at 384. The key tiles of all items of
 // a CTA form one stream: S runs two tiles and dP one tile ahead, into the next
@@ -91,21 +91,28 @@ __device__ __forceinline__ Item item_of(const WinGeo& g, int idx) {
   x.q0 = (g.n_tiles - 1 - idx / g.B) * kBM;
   return x;
 }
-// The item's key tiles, twice where a row has few keys.
+// The item's key tiles, n1 of them, and for its rows of few keys the last n2 again
+// (such a row's keys end at the diagonal; nt in all).
 constexpr int kFewKeys = 48;
 struct DqRun {
   KeyRun kr;
-  int n1, nt;  // tiles of one pass and of all
-  __device__ __forceinline__ int pass_it(int it) const { return it < n1 ? it : it - n1; }
+  int n1, n2, nt;
+  __device__ __forceinline__ int pass_it(int it) const { return it < n1 ? it : it - n2; }
   __device__ __forceinline__ int base(int it) const { return kr.base(pass_it(it)); }
   __device__ __forceinline__ int width(int it) const { return kr.width(pass_it(it)); }
 };
 __device__ __forceinline__ DqRun run_of(const WinGeo& g, const Item& x) {
   DqRun r;
-  const int qe = min(x.q0 + kBM, g.S);
+  const int qe = min(x.q0 + kBM, g.S), diag = (qe - 1) / kBN;
   r.kr = key_run(g, x.q0, qe);
-  r.n1 = r.nt = r.kr.nt;
-  if (g.W + g.ns < kFewKeys || x.q0 - r.kr.lo + 1 < kFewKeys || win_lo(g, qe - 1) > x.q0) r.nt *= 2;
+  r.n1 = r.kr.nt;
+  if (g.W + g.ns < kFewKeys)
+    r.n2 = r.n1;  // every row
+  else if (x.q0 - r.kr.lo + 1 < kFewKeys)
+    r.n2 = diag - r.kr.lo / kBN + 1;  // the first rows' document starts in or just before the tile
+  else
+    r.n2 = win_lo(g, qe - 1) > x.q0 ? 1 : 0;  // a document starts inside
+  r.nt = r.n1 + r.n2;
   return r;
 }
 
@@ -358,13 +365,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int q_last = min(x.q0 + kBM, g.S) - 1;
       const int first_all = max(win_lo(g, q_last), q_last - g.W + 1);
       float2 res2 = make_float2(0.f, 0.f);
-      float res = 0.f;
+      float res = 0.f, fix = 0.f;
       for (int it = 0; it < kr.nt; ++it, ++n) {
         if (it == kr.n1) {  // the second pass needs the row's residue
           ok = __all_sync(0xffffffffu, mbar_wait(&bars->r_full, item & 1, w, kSiteRes));
           if (!ok) break;
           const float* s = sRes + (item & 1) * 256 + row;
           res = s[0] + s[128];
+          // (the repeated tiles hold all keys of the rows of few, and only of those)
+          fix = g.W + g.ns < kFewKeys || i - lo + 1 < kFewKeys ? -res : 0.f;
         }
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[n & 1], (n >> 1) & 1, w, kSiteS));
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->dp_full, n & 1, w, kSiteDp));
@@ -415,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 32; c += 2) {
               const float2 y = ffma2(make_float2(__uint_as_float(rs[c]), __uint_as_float(rs[c + 1])), sl2, nl2);
-              dk[c >> 1] = pack_bf16x2(-res * ex2_approx(y.x), -res * ex2_approx(y.y));
+              dk[c >> 1] = pack_bf16x2(fix * ex2_approx(y.x), fix * ex2_approx(y.y));
             }
           }
           tmem_st16(trow + cS + cbase + half * 16, dk);
