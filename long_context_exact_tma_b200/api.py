@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import contextlib
 import functools
+import operator
 
 import torch
 
@@ -337,6 +338,16 @@ def _lse_of(t, q: torch.Tensor, shape, dev: int) -> torch.Tensor:
     return t
 
 
+def _window_size(window, sinks):
+    """The two as C ints: whole numbers, anything past 31 bits as the longest (or too many)."""
+    window, sinks = operator.index(window), operator.index(sinks)
+    if window < 1:
+        raise ValueError("window must be at least 1")
+    if sinks < 0:
+        raise ValueError("sinks must not be negative")
+    return min(window, 0x7FFFFFFF), min(sinks, 0x7FFFFFFF)
+
+
 def _window_geometry(q, k, v, window, sinks, cu_seqlens):
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [B, S, Hq, D] and k, v [B, S, Hkv, D]")
@@ -352,7 +363,7 @@ def _window_geometry(q, k, v, window, sinks, cu_seqlens):
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens must be [n_docs + 1]")
         n_docs = cu_seqlens.numel() - 1
-    return (B, S, Hq, Hkv, D, int(window), int(sinks)), n_docs, dev
+    return (B, S, Hq, Hkv, D, *_window_size(window, sinks)), n_docs, dev
 
 
 def _ws_bytes(n: int, what: str, *geometry) -> int:
@@ -430,7 +441,7 @@ def window_attn_decode(q, k_cache, v_cache, lens, window: int, sinks: int = 0, w
     ks, vs = k_cache.stride(), v_cache.stride()
     if ks[3] != 1 or vs[3] != 1:
         raise ValueError("the last dimension of the caches must be contiguous")
-    geo = (N, n, cap, Hq, Hkv, D, int(window), int(sinks))
+    geo = (N, n, cap, Hq, Hkv, D, *_window_size(window, sinks))
     need = _decode_ws(*geo)
     ctx, st = _on(dev, stream, q, k_cache, v_cache, lens, ws, out, lse)
     with ctx:
@@ -452,15 +463,17 @@ def rope_axes(xs, positions, inv_freq, axis, paired: bool = False, inverse: bool
     gradient's map. outs: where to write (may be xs: in place); else new contiguous tensors. Returns the
     list of outputs (one tensor for one tensor)."""
     single = isinstance(xs, torch.Tensor)
-    xs = (xs,) if single else tuple(xs)
-    if not xs or len(xs) > B_.USP_MAX_ROPE_JOBS:
+    xs = (xs,) if single else xs
+    n = len(xs)
+    if not 1 <= n <= B_.USP_MAX_ROPE_JOBS:
         raise ValueError(f"one to {B_.USP_MAX_ROPE_JOBS} tensors")
+    if outs is not None:
+        outs = (outs,) if single else outs
+        if len(outs) != n:
+            raise ValueError("one output per tensor")
     x0 = xs[0]
     dtype, dev = x0.dtype, x0.get_device()
     dt = _dt(x0)
-    outs = ((outs,) if single else tuple(outs)) if outs is not None else (None,) * len(xs)
-    if len(outs) != len(xs):
-        raise ValueError("one output per tensor")
     if x0.dim() != 4:
         raise ValueError("tensors must be [B, S, H, D]")
     B, S, _, D = x0.shape
@@ -468,7 +481,8 @@ def rope_axes(xs, positions, inv_freq, axis, paired: bool = False, inverse: bool
     if pos_type is not torch.int64 and pos_type is not torch.int32:
         raise TypeError("positions must be int32 or int64")
     _check("positions", positions, dev, pos_type)
-    if positions.dim() != 3 or positions.shape[1] != B or positions.shape[2] != S:
+    pos_shape = positions.shape
+    if len(pos_shape) != 3 or pos_shape[1] != B or pos_shape[2] != S:
         raise ValueError(f"positions must be [n_axes, {B}, {S}]")
     if inv_freq.get_device() >= 0 or inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous 1-D float64 tensor on the CPU")
@@ -477,25 +491,27 @@ def rope_axes(xs, positions, inv_freq, axis, paired: bool = False, inverse: bool
     n_freq = inv_freq.numel()
     if n_freq != axis.numel():
         raise ValueError("inv_freq and axis must have one entry per frequency")
-    ctx, st = _on(dev, stream, positions, *xs, *outs)
+    ctx, st = _on(dev, stream, positions, *xs, *(outs or ()))
     with ctx:
         ys, jobs = [], []
-        for x, y in zip(xs, outs):
+        for j in range(n):
+            x = xs[j]
             if x.dim() != 4:
                 raise ValueError("tensors must be [B, S, H, D]")
             H = x.shape[2]
-            _check("x", x, dev, dtype, (B, S, H, D), contiguous=False)
+            _check("x", x, dev, dtype, (B, S, H, D), False)
             sx = x.stride()
-            if y is None:
+            if outs is None:
                 y = torch.empty_like(x, memory_format=torch.contiguous_format)
                 sy = (S * H * D, H * D, D, 1)
             else:
-                _check("out", y, dev, dtype, (B, S, H, D), contiguous=False)
+                y = outs[j]
+                _check("out", y, dev, dtype, (B, S, H, D), False)
                 sy = y.stride()
-            if (sx[3] != 1 or sy[3] != 1) and D > 1:
+            if D > 1 and (sx[3] != 1 or sy[3] != 1):
                 raise ValueError("the last dimension must be contiguous")
             ys.append(y)
             jobs.append((x, y, H, sx[:3], sy[:3]))
-        B_.usp_rope_axes(jobs, B, S, D, 2 * n_freq, dt, positions, 64 if pos_type is torch.int64 else 32,
-                         positions.shape[0], inv_freq, axis, paired, inverse, st)
+        B_.usp_rope_axes(jobs, B, S, D, 2 * n_freq, dt, positions, 64 if pos_type is torch.int64 else 32, pos_shape[0],
+                         inv_freq, axis, paired, inverse, st)
     return ys[0] if single else ys

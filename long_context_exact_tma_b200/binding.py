@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libusp.so")
@@ -65,6 +66,9 @@ class RopeJob(ctypes.Structure):
                 ("d_b", ctypes.c_longlong), ("d_t", ctypes.c_longlong), ("d_h", ctypes.c_longlong)]
 
 
+_ROPE_JOB = struct.Struct("@PPi6q")  # the same, as bytes
+
+
 class PermuteJob(ctypes.Structure):
     """usp_permute_job of include/usp.h."""
     _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("H", ctypes.c_int), ("D", ctypes.c_int),
@@ -102,7 +106,7 @@ SIGNATURES = {
     "usp_window_attn_bwd": (_I, [_P] * 9 + [_I] * 7 + [_P, _I, _P, _SZ, _P]),
     "usp_window_decode_workspace_size": (_SZ, [_I] * 8),
     "usp_window_attn_decode": (_I, [_P] * 6 + [_I] * 8 + [_LL] * 6 + [_P, _SZ, _P]),
-    "usp_rope_axes": (_I, [ctypes.POINTER(RopeJob)] + [_I] * 6 + [_P, _I, _I, _P, _P, _I, _I, _P]),
+    "usp_rope_axes": (_I, [_P] + [_I] * 6 + [_P, _I, _I, _P, _P, _I, _I, _P]),
     "usp_rows_copy": (_I, [ctypes.POINTER(RowsJob), _I, _P]),
     "usp_longnet_rows": (_I, [_I] * 5 + [_P] * 4),
     "usp_longnet_workspace_size": (_SZ, [_I] * 5 + [_P, _P, _I]),
@@ -336,7 +340,8 @@ def usp_rope_axes(jobs, B, S, D, R, dtype, positions, pos_bits, n_axes, inv_freq
                   check=True):
     """jobs: sequence of (src, dst, H, (s_b, s_t, s_h), (d_b, d_t, d_h)); inv_freq (float64) and axis (int32) in
     host memory: CPU tensors or addresses."""
-    arr = (RopeJob * max(len(jobs), 1))(*[(_ptr(src), _ptr(dst), H, *ss, *ds) for src, dst, H, ss, ds in jobs])
+    # (packed by hand: ctypes structures would take longer to fill than the launch itself)
+    arr = b"".join([_ROPE_JOB.pack(_ptr(src) or 0, _ptr(dst) or 0, H, *ss, *ds) for src, dst, H, ss, ds in jobs])
     rc = lib().usp_rope_axes(arr, len(jobs), B, S, D, R, dtype, _ptr(positions), pos_bits, n_axes, _ptr(inv_freq),
                              _ptr(axis), int(paired), int(inverse), _stream(stream))
     return _check(rc) if check else rc

@@ -131,8 +131,7 @@ extern "C" int usp_window_attn_bwd(const void* q, const void* k, const void* v, 
   L.far_sum = has_far(L.g) ? L.far_part + far_part_floats(L.g, D) : nullptr;
   L.status = static_cast<int*>(workspace);
   L.wait_ns = current_wait_ns();
-  cudaError_t e = cudaMemsetAsync(workspace, 0, kStatusBytes, st);
-  if (e == cudaSuccess) e = launch_window_prep(L, out, lse, st);
+  cudaError_t e = launch_window_prep(L, out, lse, st);
   if (e == cudaSuccess) e = launch_window_dq(L, st);
   if (e == cudaSuccess && L.far_sum) e = launch_window_far(L, st);
   if (e == cudaSuccess) e = launch_window_dkdv(L, st);

@@ -112,10 +112,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   let_next_start();
-  wait_for_previous();
   if (threadIdx.x == 0) {
     feed_init(bars->feed, 1 + kComputeWarps);
-    bars->abort_flag = *reinterpret_cast<volatile int*>(a.status) != 0;
     mbar_init(&bars->kv_full, 1);
     mbar_init(&bars->kv_empty, 1);
     for (int s = 0; s < C::kStages; ++s) {
@@ -132,6 +130,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(&bars->tmem_base, kTmemCols);
+  wait_for_previous();
+  if (threadIdx.x == 0) bars->abort_flag = *reinterpret_cast<volatile int*>(a.status) != 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -190,9 +190,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (*reinterpret_cast<volatile int*>(&bars->abort_flag)) {
-      if (n_kv > 0) mbar_wait_drain(&bars->kv_full, (n_kv - 1) & 1, a.wait_ns);
+      if (n_kv > 0) mbar_wait_drain(&bars->kv_full, (n_kv - 1) & 1, kDrainNs);
       for (int it = issued - C::kStages < 0 ? 0 : issued - C::kStages; it < issued; ++it)
-        mbar_wait_drain(&bars->qd_full[it % C::kStages], (it / C::kStages) & 1, a.wait_ns);
+        mbar_wait_drain(&bars->qd_full[it % C::kStages], (it / C::kStages) & 1, kDrainNs);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok && issued_any) {
       umma_commit_w(&bars->drain);
-      mbar_wait_drain(&bars->drain, 0, a.wait_ns);
+      mbar_wait_drain(&bars->drain, 0, kDrainNs);
     }
     __syncwarp();
   } else {

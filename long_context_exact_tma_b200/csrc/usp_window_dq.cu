@@ -103,15 +103,13 @@ struct DqRun {
 };
 __device__ __forceinline__ DqRun run_of(const WinGeo& g, const Item& x) {
   DqRun r;
-  const int qe = min(x.q0 + kBM, g.S), diag = (qe - 1) / kBN;
+  const int qe = min(x.q0 + kBM, g.S);
   r.kr = key_run(g, x.q0, qe);
   r.n1 = r.kr.nt;
-  if (g.W + g.ns < kFewKeys)
-    r.n2 = r.n1;  // every row
-  else if (x.q0 - r.kr.lo + 1 < kFewKeys)
-    r.n2 = diag - r.kr.lo / kBN + 1;  // the first rows' document starts in or just before the tile
+  if (g.W + g.ns < kFewKeys || x.q0 - r.kr.lo + 1 < kFewKeys)
+    r.n2 = r.n1;  // every row, or a document that starts in or just before the tile: two or three tiles
   else
-    r.n2 = win_lo(g, qe - 1) > x.q0 ? 1 : 0;  // a document starts inside
+    r.n2 = win_lo(g, qe - 1) > x.q0 ? 1 : 0;  // documents that start inside: the diagonal tile
   r.nt = r.n1 + r.n2;
   return r;
 }
@@ -138,10 +136,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   let_next_start();
-  wait_for_previous();
   if (threadIdx.x == 0) {
     feed_init(bars->feed, 1 + kComputeWarps);
-    bars->abort_flag = *reinterpret_cast<volatile int*>(a.status) != 0;
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
     mbar_init(&bars->do_full, 1);
@@ -164,6 +160,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(&bars->tmem_base, kTmemCols);
+  wait_for_previous();
+  if (threadIdx.x == 0) bars->abort_flag = *reinterpret_cast<volatile int*>(a.status) != 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -213,12 +211,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (*reinterpret_cast<volatile int*>(&bars->abort_flag)) {
-      if (n_q > 0) mbar_wait_drain(&bars->q_full, (n_q - 1) & 1, a.wait_ns);
-      if (n_do > 0) mbar_wait_drain(&bars->do_full, (n_do - 1) & 1, a.wait_ns);
+      if (n_q > 0) mbar_wait_drain(&bars->q_full, (n_q - 1) & 1, kDrainNs);
+      if (n_do > 0) mbar_wait_drain(&bars->do_full, (n_do - 1) & 1, kDrainNs);
       for (int it = nk - C::kKSt < 0 ? 0 : nk - C::kKSt; it < nk; ++it)
-        mbar_wait_drain(&bars->k_full[it % C::kKSt], (it / C::kKSt) & 1, a.wait_ns);
+        mbar_wait_drain(&bars->k_full[it % C::kKSt], (it / C::kKSt) & 1, kDrainNs);
       for (int it = nv - C::kVSt < 0 ? 0 : nv - C::kVSt; it < nv; ++it)
-        mbar_wait_drain(&bars->v_full[it % C::kVSt], (it / C::kVSt) & 1, a.wait_ns);
+        mbar_wait_drain(&bars->v_full[it % C::kVSt], (it / C::kVSt) & 1, kDrainNs);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -336,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok && issued_any) {
       umma_commit_w(&bars->drain);
-      mbar_wait_drain(&bars->drain, 0, a.wait_ns);
+      mbar_wait_drain(&bars->drain, 0, kDrainNs);
     }
     __syncwarp();
   } else {

@@ -237,9 +237,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (*reinterpret_cast<volatile int*>(&bars->abort_flag)) {
       // let every copy this warp started land before the CTA exits
-      if (n_q > 0) mbar_wait_drain(&bars->q_full, (n_q - 1) & 1, a.wait_ns);
+      if (n_q > 0) mbar_wait_drain(&bars->q_full, (n_q - 1) & 1, kDrainNs);
       for (int it = issued - n_st < 0 ? 0 : issued - n_st; it < issued; ++it)
-        mbar_wait_drain(&full[it % n_st], (it / n_st) & 1, a.wait_ns);
+        mbar_wait_drain(&full[it % n_st], (it / n_st) & 1, kDrainNs);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok && issued_any) {
       umma_commit_w(&bars->drain);
-      mbar_wait_drain(&bars->drain, 0, a.wait_ns);
+      mbar_wait_drain(&bars->drain, 0, kDrainNs);
     }
     __syncwarp();
   } else {

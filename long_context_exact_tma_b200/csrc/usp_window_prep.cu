@@ -1,6 +1,7 @@
 // usp_window_prep.cu -- the row tables of the window backward: -LSE*log2(e) and
 // -Delta = -sum_d dO_d O_d, per head ([B*Hq][Lp], Lp = S rounded up to 128; -inf
-// and 0 on the padding rows, whose weights then are 0).
+// and 0 on the padding rows, whose weights then are 0). The backward's first kernel:
+// it also clears the workspace header (status word, item counters).
 //
 // Bound by reading O and dO once. Neighbouring lanes read neighbouring 16 bytes
 // (D/8 lanes make a row), and a warp asks for all of its 8 or 16 rows before it
@@ -20,11 +21,13 @@ template <int D>
 __global__ void __launch_bounds__(kThreads) window_prep_kernel(const uint4* __restrict__ out,
                                                                const uint4* __restrict__ dO,
                                                                const float* __restrict__ lse, float* __restrict__ lse2_t,
-                                                               float* __restrict__ delta_t, long long rows, int S,
+                                                               float* __restrict__ delta_t,
+                                                               int* __restrict__ header, long long rows, int S,
                                                                int Hq, int Lp, long long pad_rows) {
   constexpr int kLanes = D / 8;              // lanes of a row
   constexpr int kRows = 32 / kLanes;         // rows of a step
   let_next_start();
+  if (blockIdx.x == 0 && threadIdx.x < kStatusBytes / 4) header[threadIdx.x] = 0;
   const int lane = threadIdx.x & 31;
   const long long warp = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
   const long long r0 = warp * (kRows * kSteps) + lane / kLanes;
@@ -78,7 +81,7 @@ cudaError_t launch_d(const WinLaunch& L, const void* out, const float* lse, cuda
   const long long per_block = kThreads / (D / 8) * kSteps;
   const unsigned blocks = static_cast<unsigned>((rows + per_block - 1) / per_block);
   window_prep_kernel<D><<<blocks, kThreads, 0, stream>>>(
-      static_cast<const uint4*>(out), static_cast<const uint4*>(L.dO), lse, L.lse2, L.delta, rows, L.g.S, L.g.Hq, L.Lp,
+      static_cast<const uint4*>(out), static_cast<const uint4*>(L.dO), lse, L.lse2, L.delta, L.status, rows, L.g.S, L.g.Hq, L.Lp,
       static_cast<long long>(L.g.B) * L.g.Hq * (L.Lp - L.g.S));
   note_launch();
   return cudaGetLastError();

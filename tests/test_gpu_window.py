@@ -39,6 +39,9 @@ CASES = [
     (1, 1300, 3, 3, 64, 200, 3, [0, 100, 1290, 1300]),
     (1, 1024, 2, 2, 64, 50, 128, [0, 384, 512, 1024]),
     (1, 900, 8, 1, 128, 400, 4, list(range(0, 901, 9))),         # documents shorter than a tile
+    (1, 500, 2, 2, 64, 1, 100, [0, 88, 500]),                    # two sink tiles of rows of few keys
+    (2, 777, 3, 1, 128, 300, 70, [0, 500, 777]),                 # row pairs whose second tile starts behind the sinks
+    (1, 650, 1, 1, 64, 140, 5, [0, 129, 300, 650]),
 ]
 
 

@@ -137,6 +137,13 @@ def test_python_calls_refuse_cpu_tensors_and_types():
         api.window_attn_decode(x, x, x, x, 4)
     with pytest.raises(ValueError):
         api.window_attn_fwd(x[0], x, x, 4)
+    with pytest.raises(ValueError):
+        api._window_size(0, 1)
+    with pytest.raises(ValueError):
+        api._window_size(1, -1)
+    with pytest.raises(TypeError):
+        api._window_size(3.5, 0)
+    assert api._window_size(1 << 40, 1 << 35) == (0x7FFFFFFF, 0x7FFFFFFF)
     inv, axis = torch.ones(4, dtype=torch.float64), torch.zeros(4, dtype=torch.int32)
     with pytest.raises(ValueError):
         api.rope_axes(x, torch.zeros((1, 1, 8), dtype=torch.int64), inv, axis)
@@ -147,4 +154,6 @@ def test_python_calls_refuse_cpu_tensors_and_types():
 
 
 def test_rope_job_matches_the_header():
-    assert ctypes.sizeof(B_.RopeJob) == 8 + 8 + 8 + 6 * 8
+    assert ctypes.sizeof(B_.RopeJob) == 8 + 8 + 8 + 6 * 8 == B_._ROPE_JOB.size
+    job = B_.RopeJob(1, 2, 3, 4, 5, 6, 7, 8, 9)
+    assert bytes(job) == B_._ROPE_JOB.pack(1, 2, 3, 4, 5, 6, 7, 8, 9)
