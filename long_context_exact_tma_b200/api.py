@@ -349,14 +349,18 @@ def _window_size(window, sinks):
 
 
 def _window_geometry(q, k, v, window, sinks, cu_seqlens):
-    if q.dim() != 4 or k.dim() != 4:
+    dev, qs, ks = q.get_device(), q.shape, k.shape
+    if len(qs) != 4 or len(ks) != 4:
         raise ValueError("q must be [B, S, Hq, D] and k, v [B, S, Hkv, D]")
-    B, S, Hq, D = q.shape
-    Hkv = k.shape[2]
-    dev = q.get_device()
-    _check("q", q, dev, torch.bfloat16)
-    _check("k", k, dev, torch.bfloat16, (B, S, Hkv, D))
-    _check("v", v, dev, torch.bfloat16, (B, S, Hkv, D))
+    B, S, Hq, D = qs
+    Hkv = ks[2]
+    bf16 = torch.bfloat16
+    if not (dev >= 0 and k.get_device() == dev and v.get_device() == dev and q.dtype is bf16 and k.dtype is bf16
+            and v.dtype is bf16 and ks[0] == B and ks[1] == S and ks[3] == D and v.shape == ks and q.is_contiguous()
+            and k.is_contiguous() and v.is_contiguous()):
+        _check("q", q, dev, bf16)
+        _check("k", k, dev, bf16, (B, S, Hkv, D))
+        _check("v", v, dev, bf16, (B, S, Hkv, D))
     n_docs = 0
     if cu_seqlens is not None:
         _check("cu_seqlens", cu_seqlens, dev, torch.int32)
@@ -396,7 +400,8 @@ def window_attn_fwd(q, k, v, window: int, sinks: int = 0, cu_seqlens=None, ws=No
         out = _like(out, "out", q, dev)
         lse = _lse_of(lse, q, geo[:3], dev)
         ws = _scratch(ws, need, q, dev)
-        B_.usp_window_attn_fwd(q, k, v, out, lse, *geo, cu_seqlens, n_docs, ws, ws.numel(), st)
+        B_.call("usp_window_attn_fwd", q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), *geo,
+                None if cu_seqlens is None else cu_seqlens.data_ptr(), n_docs, ws.data_ptr(), ws.numel(), st)
         if check_status:
             check_workspace(ws, st)
     return out, lse
@@ -416,7 +421,9 @@ def window_attn_bwd(q, k, v, out, lse, dO, window: int, sinks: int = 0, cu_seqle
         dk = _like(dk, "dk", k, dev)
         dv = _like(dv, "dv", v, dev)
         ws = _scratch(ws, need, q, dev)
-        B_.usp_window_attn_bwd(q, k, v, out, lse, dO, dq, dk, dv, *geo, cu_seqlens, n_docs, ws, ws.numel(), st)
+        B_.call("usp_window_attn_bwd", q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                dO.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *geo,
+                None if cu_seqlens is None else cu_seqlens.data_ptr(), n_docs, ws.data_ptr(), ws.numel(), st)
         if check_status:
             check_workspace(ws, st)
     return dq, dk, dv
@@ -429,14 +436,18 @@ def window_attn_decode(q, k_cache, v_cache, lens, window: int, sinks: int = 0, w
     them, lens [N] int32 (CUDA) tokens each. Returns (out bf16 like q, lse fp32 [N, n, Hq]); a token at
     a negative position (lens < n: an idle slot) gets out = 0, lse = -inf. Cache rows past lens are
     never read."""
-    if q.dim() != 4 or k_cache.dim() != 4:
+    dev, qs, cs = q.get_device(), q.shape, k_cache.shape
+    if len(qs) != 4 or len(cs) != 4:
         raise ValueError("q must be [N, n, Hq, D] and the caches [N, cap, Hkv, D]")
-    N, n, Hq, D = q.shape
-    cap, Hkv = k_cache.shape[1], k_cache.shape[2]
-    dev = q.get_device()
-    _check("q", q, dev, torch.bfloat16)
-    _check("k_cache", k_cache, dev, torch.bfloat16, (N, cap, Hkv, D), contiguous=False)
-    _check("v_cache", v_cache, dev, torch.bfloat16, (N, cap, Hkv, D), contiguous=False)
+    N, n, Hq, D = qs
+    _, cap, Hkv, _ = cs
+    bf16 = torch.bfloat16
+    if not (dev >= 0 and k_cache.get_device() == dev and v_cache.get_device() == dev and q.dtype is bf16
+            and k_cache.dtype is bf16 and v_cache.dtype is bf16 and cs[0] == N and cs[3] == D and v_cache.shape == cs
+            and q.is_contiguous()):
+        _check("q", q, dev, bf16)
+        _check("k_cache", k_cache, dev, bf16, (N, cap, Hkv, D), False)
+        _check("v_cache", v_cache, dev, bf16, (N, cap, Hkv, D), False)
     _check("lens", lens, dev, torch.int32, (N,))
     ks, vs = k_cache.stride(), v_cache.stride()
     if ks[3] != 1 or vs[3] != 1:
@@ -449,8 +460,9 @@ def window_attn_decode(q, k_cache, v_cache, lens, window: int, sinks: int = 0, w
         lse = _lse_of(lse, q, (N, n, Hq), dev)
         # (the smallest size: the splits join in the launch itself and need none)
         ws = _scratch(ws, need, q, dev) if ws is not None or need > 256 else None
-        B_.usp_window_attn_decode(q, k_cache, v_cache, lens, out, lse, *geo, ks[:3], vs[:3], ws,
-                                  0 if ws is None else ws.numel(), st)
+        B_.call("usp_window_attn_decode", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), lens.data_ptr(),
+                out.data_ptr(), lse.data_ptr(), *geo, *ks[:3], *vs[:3], None if ws is None else ws.data_ptr(),
+                0 if ws is None else ws.numel(), st)
     return out, lse
 
 
@@ -502,7 +514,8 @@ def rope_axes(xs, positions, inv_freq, axis, paired: bool = False, inverse: bool
             _check("x", x, dev, dtype, (B, S, H, D), False)
             sx = x.stride()
             if outs is None:
-                y = torch.empty_like(x, memory_format=torch.contiguous_format)
+                y = (torch.empty_like(x) if x.is_contiguous()
+                     else torch.empty_like(x, memory_format=torch.contiguous_format))
                 sy = (S * H * D, H * D, D, 1)
             else:
                 y = outs[j]
@@ -511,7 +524,8 @@ def rope_axes(xs, positions, inv_freq, axis, paired: bool = False, inverse: bool
             if D > 1 and (sx[3] != 1 or sy[3] != 1):
                 raise ValueError("the last dimension must be contiguous")
             ys.append(y)
-            jobs.append((x, y, H, sx[:3], sy[:3]))
-        B_.usp_rope_axes(jobs, B, S, D, 2 * n_freq, dt, positions, 64 if pos_type is torch.int64 else 32, pos_shape[0],
-                         inv_freq, axis, paired, inverse, st)
+            jobs.append(B_.ROPE_JOB.pack(x.data_ptr(), y.data_ptr(), H, *sx[:3], *sy[:3]))
+        B_.call("usp_rope_axes", b"".join(jobs), n, B, S, D, 2 * n_freq, dt, positions.data_ptr(),
+                64 if pos_type is torch.int64 else 32, pos_shape[0], inv_freq.data_ptr(), axis.data_ptr(),
+                1 if paired else 0, 1 if inverse else 0, st)
     return ys[0] if single else ys

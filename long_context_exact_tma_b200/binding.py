@@ -66,7 +66,7 @@ class RopeJob(ctypes.Structure):
                 ("d_b", ctypes.c_longlong), ("d_t", ctypes.c_longlong), ("d_h", ctypes.c_longlong)]
 
 
-_ROPE_JOB = struct.Struct("@PPi6q")  # the same, as bytes
+ROPE_JOB = struct.Struct("@PPi6q")  # the same, as bytes
 
 
 class PermuteJob(ctypes.Structure):
@@ -179,6 +179,14 @@ def _check(rc: int) -> int:
     if rc != USP_OK:
         raise UspError(rc, lib().usp_last_error().decode())
     return rc
+
+
+def call(name: str, *args) -> None:
+    """The C call of that name with addresses and numbers as they are (for callers that have them at
+    hand: on a call of a few microseconds the functions below cost one more); raises on a bad status."""
+    rc = getattr(_lib or lib(), name)(*args)
+    if rc != USP_OK:
+        _check(rc)
 
 
 def usp_version() -> int:
@@ -341,7 +349,7 @@ def usp_rope_axes(jobs, B, S, D, R, dtype, positions, pos_bits, n_axes, inv_freq
     """jobs: sequence of (src, dst, H, (s_b, s_t, s_h), (d_b, d_t, d_h)); inv_freq (float64) and axis (int32) in
     host memory: CPU tensors or addresses."""
     # (packed by hand: ctypes structures would take longer to fill than the launch itself)
-    arr = b"".join([_ROPE_JOB.pack(_ptr(src) or 0, _ptr(dst) or 0, H, *ss, *ds) for src, dst, H, ss, ds in jobs])
+    arr = b"".join([ROPE_JOB.pack(_ptr(src) or 0, _ptr(dst) or 0, H, *ss, *ds) for src, dst, H, ss, ds in jobs])
     rc = lib().usp_rope_axes(arr, len(jobs), B, S, D, R, dtype, _ptr(positions), pos_bits, n_axes, _ptr(inv_freq),
                              _ptr(axis), int(paired), int(inverse), _stream(stream))
     return _check(rc) if check else rc

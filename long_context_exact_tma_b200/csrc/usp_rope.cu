@@ -232,6 +232,18 @@ cudaError_t launch(RopeArgs& a, long long tokens, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+// inv_freq / 2 pi modulo 1 as a fraction of 2^64, to about 2^-64 of it (relative): the product
+// with 1 / 2 pi in two doubles, whole turns per position step dropped.
+unsigned long long turn_of(double inv_freq) {
+  if (inv_freq < 0) return 0ull - turn_of(-inv_freq);
+  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;  // 1 / 2 pi and what its double leaves out
+  const double hi = inv_freq * kHi, lo = fma(inv_freq, kHi, -hi) + inv_freq * kLo;
+  const double frac = hi - floor(hi);           // exact
+  const double up = floor(frac * 4294967296.0), rest = frac * 4294967296.0 - up;  // upper 32 bits, and the rest of them
+  const long long low = static_cast<long long>((rest + lo * 4294967296.0) * 4294967296.0);  // may be just below 0
+  return (static_cast<unsigned long long>(up) << 32) + static_cast<unsigned long long>(low);
+}
+
 }  // namespace
 }  // namespace usp
 
@@ -293,10 +305,7 @@ extern "C" int usp_rope_axes(const usp_rope_job* jobs, int n_jobs, int B, int S,
   for (int f = 0; f < R / 2; ++f) {
     if (!isfinite(inv_freq[f])) return record_error(USP_ERR_INVALID_ARG, "inv_freq[%d] is not finite", f);
     if (axis[f] < 0 || axis[f] >= n_axes) return record_error(USP_ERR_INVALID_ARG, "axis[%d] = %d is outside 0..%d", f, axis[f], n_axes - 1);
-    const long double turns = static_cast<long double>(inv_freq[f]) * 0.159154943091895335768883763372514362L;
-    // [0, 1): whole turns per position step do nothing
-    const long double frac = turns >= 0.0L && turns < 1.0L ? turns : turns - floorl(turns);
-    a.turn[f] = frac >= 1.0L ? 0ull : static_cast<unsigned long long>(frac * 18446744073709551616.0L);
+    a.turn[f] = turn_of(inv_freq[f]);
     a.axis[f] = static_cast<unsigned char>(axis[f]);
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -154,6 +154,6 @@ def test_python_calls_refuse_cpu_tensors_and_types():
 
 
 def test_rope_job_matches_the_header():
-    assert ctypes.sizeof(B_.RopeJob) == 8 + 8 + 8 + 6 * 8 == B_._ROPE_JOB.size
+    assert ctypes.sizeof(B_.RopeJob) == 8 + 8 + 8 + 6 * 8 == B_.ROPE_JOB.size
     job = B_.RopeJob(1, 2, 3, 4, 5, 6, 7, 8, 9)
-    assert bytes(job) == B_._ROPE_JOB.pack(1, 2, 3, 4, 5, 6, 7, 8, 9)
+    assert bytes(job) == B_.ROPE_JOB.pack(1, 2, 3, 4, 5, 6, 7, 8, 9)
