@@ -231,18 +231,23 @@ struct WinLaunch {
   float *lse2, *delta;         // [B*Hq][Lp]: -LSE*log2(e), -Delta; -inf and 0 on padding rows
   int Lp;
   const void *q, *k, *v, *dO;  // the tensors behind the maps (far sinks)
-  float* far_part;             // [B][Hkv][n_tiles][ns][2][D]
-  float* far_sum;              // [B][Hkv][n_docs][ns][2][D], null without sinks
+  // dK, dV of the sinks from the queries outside their key tile's band, by runs of query
+  // tiles that start at multiples of far_chunk and where a document's first tile is:
+  // [B][Hkv][run's first tile][ns][2][D]; null without such queries
+  float* far_part;
+  int far_chunk;
+  float* far_sum;  // their sums [B][Hkv][n_docs][ns][2][D], or null: few runs
   int* status;
   unsigned long long wait_ns;
 };
 cudaError_t launch_window_fwd(const WinLaunch& L, cudaStream_t stream);
 // The backward's launches in their order: the row tables; dQ, which corrects the
-// Delta table; the sinks' far sums; dK and dV.
+// Delta table; the sinks' far partials; dK and dV.
 cudaError_t launch_window_prep(const WinLaunch& L, const void* out, const float* lse, cudaStream_t stream);
 cudaError_t launch_window_dq(const WinLaunch& L, cudaStream_t stream);
 cudaError_t launch_window_dkdv(const WinLaunch& L, cudaStream_t stream);
-// dK, dV of the sinks from the queries outside their key tile's band: far_part, then far_sum.
+int window_far_chunk(const WinGeo& g);
+bool window_far_summed(const WinGeo& g);
 cudaError_t launch_window_far(const WinLaunch& L, cudaStream_t stream);
 
 // The current device's multiprocessor count.

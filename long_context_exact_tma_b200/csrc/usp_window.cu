@@ -127,13 +127,16 @@ extern "C" int usp_window_attn_bwd(const void* q, const void* k, const void* v, 
   L.lse2 = lse2;
   L.delta = delta;
   L.Lp = L.g.n_tiles * 128;
-  L.far_part = delta + table_floats(L.g);
-  L.far_sum = has_far(L.g) ? L.far_part + far_part_floats(L.g, D) : nullptr;
+  if (has_far(L.g)) {
+    L.far_part = delta + table_floats(L.g);
+    L.far_chunk = window_far_chunk(L.g);
+    if (window_far_summed(L.g)) L.far_sum = L.far_part + far_part_floats(L.g, D);
+  }
   L.status = static_cast<int*>(workspace);
   L.wait_ns = current_wait_ns();
   cudaError_t e = launch_window_prep(L, out, lse, st);
   if (e == cudaSuccess) e = launch_window_dq(L, st);
-  if (e == cudaSuccess && L.far_sum) e = launch_window_far(L, st);
+  if (e == cudaSuccess && L.far_part) e = launch_window_far(L, st);
   if (e == cudaSuccess) e = launch_window_dkdv(L, st);
   return e == cudaSuccess ? USP_OK : record_error(USP_ERR_CUDA, "window attention backward: %s", cudaGetErrorString(e));
 }

@@ -52,6 +52,8 @@ struct Args {
   int Lp;
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
+  const float* far_part;  // see WinLaunch
+  int far_chunk;
   const float* far_sum;
   int n_items;
   int* status;
@@ -376,11 +378,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) {
         tc_fence_after();
         const size_t kv0 = (static_cast<size_t>(x.b) * g.S * g.Hkv + x.gl) * D;  // row 0 of the kv head
-        const float* far = nullptr;  // the far queries' sums of this key, dK then dV
-        if (sink >= 0 && a.far_sum) {
-          const int d = g.cu ? doc_of(g.cu, g.n_docs, j) : 0;
-          far = a.far_sum +
-                (((static_cast<size_t>(x.b) * g.Hkv + x.gl) * g.n_docs + d) * g.ns + sink) * (2 * D);
+        // the far queries' part of a sink's gradients, dK then dV: their sum, or the partials of the runs f0 .. f1,
+        // whose first tiles are multiples of the chunk or the document's first tile, from the first query tile
+        // outside the key tile's band on
+        const float* far = nullptr;
+        int f0 = 0, f1 = -1, md = 0;
+        if (sink >= 0 && a.far_part) {
+          const int mf = x.n + x.n_m, me = (hi - 1) / kBM + 1;
+          if (mf < me) {
+            const size_t bh = static_cast<size_t>(x.b) * g.Hkv + x.gl;
+            if (a.far_sum) {
+              const int d = g.cu ? doc_of(g.cu, g.n_docs, j) : 0;
+              far = a.far_sum + ((bh * g.n_docs + d) * g.ns + sink) * (2 * D);
+              f1 = 0;
+            } else {
+              far = a.far_part + (bh * g.n_tiles * g.ns + sink) * (2 * D);
+              f0 = mf / a.far_chunk;
+              f1 = (me - 1) / a.far_chunk;
+              md = (lo + kBM - 1) / kBM;
+            }
+          }
         }
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {  // dK, then dV
@@ -393,9 +410,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(trow + col + c0, r);
             tmem_ld_wait();
             reg_fence32(r);
-            if (far) {
+            for (int y = f0; y <= f1; ++y) {
+              const float4* p = reinterpret_cast<const float4*>(
+                  far + static_cast<size_t>(max(y * a.far_chunk, md)) * g.ns * (2 * D) + half * D + c0);
 #pragma unroll
-              for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) + far[half * D + c0 + c]);
+              for (int c = 0; c < 8; ++c) {
+                const float4 f4 = p[c];
+                r[4 * c] = __float_as_uint(__uint_as_float(r[4 * c]) + f4.x);
+                r[4 * c + 1] = __float_as_uint(__uint_as_float(r[4 * c + 1]) + f4.y);
+                r[4 * c + 2] = __float_as_uint(__uint_as_float(r[4 * c + 2]) + f4.z);
+                r[4 * c + 3] = __float_as_uint(__uint_as_float(r[4 * c + 3]) + f4.w);
+              }
             }
             __syncwarp();
 #pragma unroll
@@ -431,6 +456,8 @@ cudaError_t launch_d(const WinLaunch& L, cudaStream_t stream) {
   a.Lp = L.Lp;
   a.dk = static_cast<__nv_bfloat16*>(L.dk);
   a.dv = static_cast<__nv_bfloat16*>(L.dv);
+  a.far_part = L.far_part;
+  a.far_chunk = L.far_chunk;
   a.far_sum = L.far_sum;
   a.status = L.status;
   a.wait_ns = L.wait_ns;

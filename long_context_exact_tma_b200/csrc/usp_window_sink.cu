@@ -14,8 +14,10 @@
 // a run of query tiles of one document and kv head and streams its rows, tile by
 // tile and head by head; every warp fetches its own rows through its own ring of
 // cp.async buffers, so the loop has no block barrier. The warps' fp32 sums are
-// joined in a fixed order, and a second kernel adds the runs in a fixed order: no
-// atomics, the result does not depend on scheduling.
+// joined in a fixed order and written per run; the key-major kernel adds the runs of
+// each sink in order in its epilogue, or, where they are many, their sums, which a
+// second kernel makes in a fixed order. No atomics: the result does not depend on
+// scheduling.
 #include <math.h>
 
 #include "usp_mma.cuh"
@@ -35,7 +37,7 @@ struct FarArgs {
   const __nv_bfloat16 *q, *k, *v, *dO;
   const float *lse2, *delta;
   int Lp;
-  int chunk;    // tiles of a CTA: its runs start at multiples of it and where a document's tiles start
+  int chunk;  // tiles of a CTA: its runs start at multiples of it and where a document's tiles start
   int n_chunks;
   float* part;  // [b][kv head][first tile of the run][sink][2][D]
   float* sum;
@@ -252,21 +254,36 @@ cudaError_t launch_d(const WinLaunch& L, cudaStream_t stream) {
   a.delta = L.delta;
   a.Lp = L.Lp;
   a.part = L.far_part;
-  a.sum = L.far_sum;
   const long long heads = static_cast<long long>(L.g.Hkv) * L.g.B;
-  // One wave of equal CTAs while the kv heads leave several to each (a run's start and end cost some
-  // microseconds), else three, so that the last wave's idle share is small.
-  const long long sms = sm_count(), per_head = (heads <= sms / 2 ? sms : 3 * sms) / heads;
-  a.chunk = per_head > 1 ? static_cast<int>((L.g.n_tiles + per_head - 1) / per_head) : L.g.n_tiles;
+  a.chunk = L.far_chunk;
   a.n_chunks = (L.g.n_tiles + a.chunk - 1) / a.chunk;
-  const long long n_far = heads * a.n_chunks, n_sum = heads * L.g.n_docs * L.g.ns;
-  if (n_far > 0x7FFFFFFFLL || n_sum > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+  const long long n_far = static_cast<long long>(L.g.Hkv) * L.g.B * a.n_chunks;
+  if (n_far > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
   e = launch_behind(far_kernel<D>, dim3(static_cast<unsigned>(n_far)), kThreads, C::kSmemBytes, stream, a);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || !L.far_sum) return e;
+  const long long n_sum = static_cast<long long>(L.g.Hkv) * L.g.B * L.g.n_docs * L.g.ns;
+  if (n_sum > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+  a.sum = L.far_sum;
   return launch_behind(far_sum_kernel<D>, dim3(static_cast<unsigned>(n_sum)), 8 * D, 0, stream, a);
 }
 
 }  // namespace
+
+// One wave of equal CTAs while the kv heads leave several to each (a run's start and end cost some
+// microseconds), else three, so that the last wave's idle share is small.
+int window_far_chunk(const WinGeo& g) {
+  const long long heads = static_cast<long long>(g.Hkv) * g.B;
+  const long long sms = sm_count(), per_head = (heads <= sms / 2 ? sms : 3 * sms) / heads;
+  return per_head > 1 ? static_cast<int>((g.n_tiles + per_head - 1) / per_head) : g.n_tiles;
+}
+
+// Up to 8 runs the epilogue of the few key tiles with sinks adds them itself (a training step on 515
+// tokens: 48 us against 51 with the second kernel); 32 runs there cost it more than a launch (a step on
+// 8192: 291 us against 283).
+bool window_far_summed(const WinGeo& g) {
+  const int chunk = window_far_chunk(g);
+  return (g.n_tiles + chunk - 1) / chunk > 8;
+}
 
 cudaError_t launch_window_far(const WinLaunch& L, cudaStream_t stream) {
   return L.D == 128 ? launch_d<128>(L, stream) : L.D == 64 ? launch_d<64>(L, stream) : cudaErrorInvalidValue;
