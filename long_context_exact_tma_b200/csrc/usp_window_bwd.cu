@@ -16,6 +16,10 @@
 // as soon as this item's last products have read those columns, so they overlap
 // its epilogue; its dV and dK cannot overtake the epilogue's reads because they
 // wait for P^T and dS^T, which the same warps write after them.
+//
+// Bound by the chain S^T -> P^T -> dV -> S^T (1.8 us per step; the four products take
+// 1.1) and by about 6 us per item. B=1 S=32768 H=16/4 D=128 W=2048, 4 sinks: 890 us,
+// 1199 TFLOP/s (8 D flops per visible pair).
 #include <math.h>
 
 #include "usp_ptx.cuh"

@@ -18,6 +18,9 @@
 // keys of all sequences of a kv head in equal chunks (each works its share out from
 // lens; 4 conversations of 30 to 128 thousand tokens took 199 us in equal splits of
 // each), write fp32 partials, and a second kernel joins a row's by their LSE.
+//
+// 64 sequences, W=4096, H=32/8, D=128: 154 us on the device, 6.9 TB/s of visible
+// rows; 4 tokens of 4 conversations, H=32/4: 115 us and 9 us of joining.
 #include <math.h>
 
 #include "../../include/usp.h"
