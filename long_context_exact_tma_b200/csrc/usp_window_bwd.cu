@@ -117,7 +117,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const WinGeo& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  let_next_start();
   if (threadIdx.x == 0) {
     feed_init(bars->feed, 1 + kComputeWarps);
     mbar_init(&bars->kv_full, 1);
@@ -135,7 +134,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars->drain, 1);
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(&bars->tmem_base, kTmemCols);
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem_base, kTmemCols);
+    // (not before: a CTA of the next kernel must not take the columns that this one waits for)
+    let_next_start();
+  }
   wait_for_previous();
   if (threadIdx.x == 0) bars->abort_flag = *reinterpret_cast<volatile int*>(a.status) != 0;
   tc_fence_before();

@@ -70,7 +70,11 @@ struct Args {
 struct Bars {
   uint64_t q_full, q_empty, do_full, do_empty;
   uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
-  uint64_t s_full[2], dp_full, dp_free, ds_full, dq_done[2], drain;
+  uint64_t s_full[2], dp_full, dp_free, dq_done[2], drain;
+  // One per S buffer: dP of the next tile is issued ahead of the wait for dS, so the warps can
+  // finish two tiles before the issuer looks for the first one's arrivals, whose phase a single
+  // barrier would have left again by then. They cannot finish a third: its dP is issued behind.
+  uint64_t ds_full[2];
   uint64_t r_full;  // both warpgroups' residues of the item are in sRes
   ItemFeed feed;
   uint32_t tmem_base;
@@ -139,7 +143,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const WinGeo& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  let_next_start();
   if (threadIdx.x == 0) {
     feed_init(bars->feed, 1 + kComputeWarps);
     mbar_init(&bars->q_full, 1);
@@ -155,15 +158,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->v_empty[s], 1);
       mbar_init(&bars->s_full[s], 1);
       mbar_init(&bars->dq_done[s], 1);
+      mbar_init(&bars->ds_full[s], kComputeWarps);
     }
     mbar_init(&bars->dp_full, 1);
     mbar_init(&bars->dp_free, kComputeWarps);
-    mbar_init(&bars->ds_full, kComputeWarps);
     mbar_init(&bars->r_full, kComputeWarps);
     mbar_init(&bars->drain, 1);
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(&bars->tmem_base, kTmemCols);
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem_base, kTmemCols);
+    // (not before: a CTA of the next kernel must not take the columns that this one waits for)
+    let_next_start();
+  }
   wait_for_previous();
   if (threadIdx.x == 0) bars->abort_flag = *reinterpret_cast<volatile int*>(a.status) != 0;
   tc_fence_before();
@@ -276,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     auto issue_dq = [&](int keys, bool first) -> bool {  // dQ += dS K
-      if (!mbar_wait_w(&bars->ds_full, q_turn & 1, w, kSiteDs)) return false;
+      if (!mbar_wait_w(&bars->ds_full[q_turn & 1], (q_turn >> 1) & 1, w, kSiteDs)) return false;
       tc_fence_after();
       const uint64_t kd = dKmn + ((k_q.at * C::kTileBytes) >> 4);
       const uint32_t ds = tmem + col_s(q_turn & 1);
@@ -435,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         if (it + 1 == kr.n1) mbar_arrive_warp(&bars->r_full);
-        mbar_arrive_warp(&bars->ds_full);
+        mbar_arrive_warp(&bars->ds_full[n & 1]);
       }
       if (ok && kr.nt == kr.n1) {
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->r_full, item & 1, w, kSiteRes));

@@ -1,6 +1,7 @@
 """Sliding-window attention with sinks on a B200: forward, backward and the decode form against the
 64-bit definition, with the bounds of window_ref.py; documents, odd sizes, graphs, streams, caches."""
 import math
+import random
 
 import pytest
 import torch
@@ -61,6 +62,39 @@ def test_forward_and_backward(B, S, Hq, Hkv, D, W, ns, cu, cuda):
         assert within(x, y, t) <= 1, name
     again = api.window_attn_bwd(q, k, v, out, lse, do, W, ns, cu_seqlens=cut)
     assert all(torch.equal(x, y) for x, y in zip(got, again))
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_drawn_shapes(seed, cuda):
+    """Shapes, windows, sinks and documents drawn over the whole range, the bounds of the listed ones."""
+    rng = random.Random(seed)
+    for n in range(8):
+        D, Hkv, B = rng.choice([64, 128]), rng.choice([1, 2, 3]), rng.choice([1, 2])
+        Hq = Hkv * rng.choice([1, 2, 3, 4, 5])
+        S, W = int(math.exp(rng.uniform(0, math.log(900)))), int(math.exp(rng.uniform(0, math.log(1000))))
+        ns = rng.choice([0, 1, 4, rng.randint(0, 128), 128])
+        cu = sorted([0, S] + [rng.randint(0, S) for _ in range(rng.randint(1, 8))]) if rng.random() < 0.5 else None
+        try:
+            test_forward_and_backward(B, S, Hq, Hkv, D, W, ns, cu, cuda)
+        except AssertionError as e:
+            raise AssertionError((B, S, Hq, Hkv, D, W, ns, cu)) from e
+
+
+def test_many_short_steps_in_a_row(cuda):
+    """Items that are mostly tiles of 16 and 32 sinks, each walked twice, call after call between other
+    work: steps short enough for the warps to be two tiles ahead of a delayed product warp. Every call
+    ends, and with the first one's result."""
+    B, S, Hq, Hkv, D, W, ns = 1, 1500, 4, 2, 64, 1, 128
+    cu = torch.tensor([0, 700, 1500], dtype=torch.int32, device="cuda")
+    q, k, v = qkv(B, S, Hq, Hkv, D, seed=51)
+    do = normal(54, B, S, Hq, D)
+    out, lse = api.window_attn_fwd(q, k, v, W, ns, cu_seqlens=cu, check_status=True)
+    first = api.window_attn_bwd(q, k, v, out, lse, do, W, ns, cu_seqlens=cu, check_status=True)
+    other = torch.randn(512, 512, dtype=torch.float64, device="cuda")
+    for _ in range(300):
+        other @ other
+        got = api.window_attn_bwd(q, k, v, out, lse, do, W, ns, cu_seqlens=cu, check_status=True)
+        assert all(torch.equal(x, y) for x, y in zip(first, got))
 
 
 def test_gradients_against_differences(cuda):
