@@ -414,12 +414,12 @@ int usp_dilated_attn_fwd(const void* q, const void* k, const void* v, void* out,
  *   workspace    usp_window_workspace_size(..., n_docs, bwd) bytes (n_docs = 0
  *                without documents): the status header; for the backward also the
  *                row tables and the sums of the sinks' gradients
- * Any S >= 1; D in {64, 128}; scale 1/sqrt(D). Elements must be finite, those of
+ * S from 1 to 2^30; D in {64, 128}; scale 1/sqrt(D). Elements must be finite, those of
  * hidden keys too (a hidden key has weight 0, and 0 times infinity is NaN).
  *
  * usp_window_attn_bwd: the gradients, from the forward's out and lse: dQ, dK, dV
  * in bf16, each element its fp32 sum rounded once (dK, dV summed over the heads of
- * a group). Overwritten, deterministic.
+ * a group). Overwritten, deterministic. No output may overlap an input or another output.
  */
 #define USP_WINDOW_MAX_SINKS 128
 size_t usp_window_workspace_size(int B, int S, int Hq, int Hkv, int D, int window, int sinks, int n_docs, int bwd);
@@ -439,6 +439,7 @@ int usp_window_attn_bwd(const void* q, const void* k, const void* v, const void*
  *                s * k_sn + j * k_st + h * k_sh elements (v alike): [N][cap][Hkv][D],
  *                [N][Hkv][cap][D] or a slice of such; strides multiples of 8
  *                elements, rows of D contiguous elements
+ *                (cap up to 2^30)
  *   lens         DEVICE int32 [N], cached tokens 0 .. cap (values outside are
  *                taken as the nearer end); rows past lens are never read
  *   out          [N][n][Hq][D] bf16;  lse [N][n][Hq] fp32. A token at a negative
@@ -464,8 +465,9 @@ int usp_window_attn_decode(const void* q, const void* k_cache, const void* v_cac
  *                (e.g. q and k): row of head h, token t, sequence b at
  *                b * s_b + t * s_t + h * s_h elements of src (so a slice of a fused
  *                projection, or a broadcast by stride 0), likewise d_* of dst; rows
- *                of D contiguous elements. dst may be src with the same strides;
- *                any other overlap is undefined.
+ *                of D contiguous elements. dst may be src with the same strides
+ *                (other strides, or one job's dst as another's src or dst, are
+ *                refused; any other overlap is undefined).
  *   dtype        USP_BF16 or USP_F32 (arithmetic in fp32, rounded once)
  *   positions    DEVICE integers [n_axes][B][S], 32 or 64 bits (pos_bits); any sign
  *   inv_freq     HOST [R/2], radians per position step, finite

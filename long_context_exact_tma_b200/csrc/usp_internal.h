@@ -247,6 +247,7 @@ cudaError_t launch_window_prep(const WinLaunch& L, const void* out, const float*
 cudaError_t launch_window_dq(const WinLaunch& L, cudaStream_t stream);
 cudaError_t launch_window_dkdv(const WinLaunch& L, cudaStream_t stream);
 int window_far_chunk(const WinGeo& g);
+bool window_far_summable(const WinGeo& g);
 bool window_far_summed(const WinGeo& g);
 cudaError_t launch_window_far(const WinLaunch& L, cudaStream_t stream);
 

@@ -246,6 +246,24 @@ unsigned long long turn_of(double inv_freq) {
   return (static_cast<unsigned long long>(up) << 32) + static_cast<unsigned long long>(low);
 }
 
+// Whether rows of D elements at b * sb + t * st + h * sh may share elements: each step, the smallest
+// first, must be past the rows within it.
+bool rows_overlap(int D, int B, long long sb, int S, long long st, int H, long long sh) {
+  long long n[3] = {B, S, H}, s[3] = {sb, st, sh}, extent = D;
+  for (int x = 0; x < 3; ++x)
+    if (n[x] == 1) s[x] = 0;
+  for (int round = 0; round < 3; ++round) {
+    int at = -1;
+    for (int x = 0; x < 3; ++x)
+      if (n[x] > 1 && (at < 0 || s[x] < s[at])) at = x;
+    if (at < 0) return false;
+    if (s[at] < extent) return true;
+    extent += (n[at] - 1) * s[at];
+    n[at] = 1;
+  }
+  return false;
+}
+
 }  // namespace
 }  // namespace usp
 
@@ -287,8 +305,13 @@ extern "C" int usp_rope_axes(const usp_rope_job* jobs, int n_jobs, int B, int S,
       wide = wide && v % V == 0;
     }
     // two rows of the output must not share elements (an input may be broadcast by stride 0)
-    if ((B > 1 && j.d_b < D) || (S > 1 && j.d_t < D) || (j.H > 1 && j.d_h < D))
+    if (rows_overlap(D, B, j.d_b, S, j.d_t, j.H, j.d_h))
       return record_error(USP_ERR_INVALID_ARG, "job %d: the output's rows overlap", x);
+    if (j.src == j.dst && (j.s_b != j.d_b || j.s_t != j.d_t || j.s_h != j.d_h))
+      return record_error(USP_ERR_INVALID_ARG, "job %d: in place with other strides", x);
+    for (int y = 0; y < x; ++y)  // the jobs run side by side
+      if (j.dst == a.job[y].dst || j.dst == a.job[y].src || j.src == a.job[y].dst)
+        return record_error(USP_ERR_INVALID_ARG, "jobs %d and %d: one writes what the other uses", y, x);
     a.job[x].src = j.src;
     a.job[x].dst = j.dst;
     a.job[x].H = j.H;

@@ -21,8 +21,8 @@ int check_shape(int B, int S, int Hq, int Hkv, int D, int window, int sinks, con
   if (Hq % Hkv != 0) return record_error(USP_ERR_UNSUPPORTED, "Hq %% Hkv != 0");
   if (sinks > USP_WINDOW_MAX_SINKS)
     return record_error(USP_ERR_UNSUPPORTED, "at most %d sinks (got %d)", USP_WINDOW_MAX_SINKS, sinks);
-  // every query row, rounded up to whole tiles, has a 31-bit number
-  if (static_cast<long long>(B) * ((S + 127LL) / 128 * 128) * Hq >= (1LL << 31))
+  // every query row, rounded up to whole tiles, has a 31-bit number, and so has a position plus a window
+  if (S > 1 << 30 || static_cast<long long>(B) * ((S + 127LL) / 128 * 128) * Hq >= (1LL << 31))
     return record_error(USP_ERR_UNSUPPORTED, "too many rows");
   *g = WinGeo{};
   g->B = B; g->S = S; g->Hq = Hq; g->Hkv = Hkv;
@@ -44,8 +44,9 @@ size_t table_floats(const WinGeo& g) { return static_cast<size_t>(g.B) * g.Hq * 
 size_t far_part_floats(const WinGeo& g, int D) {
   return has_far(g) ? static_cast<size_t>(g.B) * g.Hkv * g.n_tiles * g.ns * 2 * D : 0;
 }
+// (none where most documents are far shorter than a tile: window_far_summed)
 size_t far_sum_floats(const WinGeo& g, int D) {
-  return has_far(g) ? static_cast<size_t>(g.B) * g.Hkv * g.n_docs * g.ns * 2 * D : 0;
+  return has_far(g) && window_far_summable(g) ? static_cast<size_t>(g.B) * g.Hkv * g.n_docs * g.ns * 2 * D : 0;
 }
 // [status][-LSE*log2e][-Delta][far partials][far sums]
 size_t bwd_ws(const WinGeo& g, int D) {

@@ -591,6 +591,7 @@ int check(int N, int n, int cap, int Hq, int Hkv, int D, int window, int sinks) 
     return record_error(USP_ERR_UNSUPPORTED, "at most %d new tokens a sequence (got %d)", USP_WINDOW_MAX_NEW, n);
   if (sinks > USP_WINDOW_MAX_SINKS)
     return record_error(USP_ERR_UNSUPPORTED, "at most %d sinks (got %d)", USP_WINDOW_MAX_SINKS, sinks);
+  if (cap > 1 << 30) return record_error(USP_ERR_UNSUPPORTED, "a cache of more than 2^30 tokens");
   if (static_cast<long long>(N) * n * Hq * 8 >= (1LL << 31)) return record_error(USP_ERR_UNSUPPORTED, "too many rows");
   return USP_OK;
 }

@@ -281,10 +281,12 @@ int window_far_chunk(const WinGeo& g) {
 
 // Up to 8 runs the epilogue of the few key tiles with sinks adds them itself (a training step on 515
 // tokens: 48 us against 51 with the second kernel); 32 runs there cost it more than a launch (a step on
-// 8192: 291 us against 283).
+// 8192: 291 us against 283). Documents of less than 32 tokens on average: few of them reach past their
+// tile's band, and the sums would make most of the workspace; the epilogue adds there too.
+bool window_far_summable(const WinGeo& g) { return g.n_docs <= 4LL * g.n_tiles; }
 bool window_far_summed(const WinGeo& g) {
   const int chunk = window_far_chunk(g);
-  return (g.n_tiles + chunk - 1) / chunk > 8;
+  return window_far_summable(g) && (g.n_tiles + chunk - 1) / chunk > 8;
 }
 
 cudaError_t launch_window_far(const WinLaunch& L, cudaStream_t stream) {

@@ -43,6 +43,7 @@ CASES = [
     (1, 500, 2, 2, 64, 1, 100, [0, 88, 500]),                    # two sink tiles of rows of few keys
     (2, 777, 3, 1, 128, 300, 70, [0, 500, 777]),                 # row pairs whose second tile starts behind the sinks
     (1, 650, 1, 1, 64, 140, 5, [0, 129, 300, 650]),
+    (1, 2500, 1, 1, 64, 90, 6, [0] + list(range(60, 560, 5)) + [2300, 2500]),   # a long document among many short ones
 ]
 
 
@@ -256,6 +257,60 @@ def test_decode(N, n, cap, Hq, Hkv, D, W, ns, cuda):
     kt, vt = (x.transpose(1, 2).contiguous().transpose(1, 2) for x in (k2, v2))
     out2, lse2 = api.window_attn_decode(q, kt, vt, cl, W, ns)
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("N,n,cap,Hq,Hkv,D,W,ns", [(5, 2, 700, 8, 2, 64, 100, 4), (2, 1, 30000, 8, 1, 128, 30000, 0)])
+def test_decode_captured_and_on_two_streams(N, n, cap, Hq, Hkv, D, W, ns, cuda):
+    """Replayed over a cache and lengths that have grown meanwhile, in one launch and with the keys shared
+    out; and two calls at once on their own streams."""
+    q, k, v = normal(61, N, n, Hq, D), normal(62, N, cap, Hkv, D), normal(63, N, cap, Hkv, D)
+    lens = torch.arange(N, dtype=torch.int32, device="cuda") * (cap // N) + 20
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = api.window_attn_decode(q, k, v, lens, W, ns)
+    for step in (0, 1, cap // 3):
+        lens.add_(step)
+        q.copy_(normal(64 + step, *q.shape))
+        graph.replay()
+        want = api.window_attn_decode(q, k, v, lens, W, ns)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        o, L, to, tl = decode_ref(q, k, v, [min(x, cap) for x in lens.tolist()], W, ns)
+        assert within(out, o, to) <= 1 and within(lse, L, tl) <= 1
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    qs = [q, normal(65, *q.shape)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for s in (0, 1):
+            got[s].append(api.window_attn_decode(qs[s], k, v, lens, W, ns, stream=streams[s]))
+    torch.cuda.synchronize()
+    for s in (0, 1):
+        want = api.window_attn_decode(qs[s], k, v, lens, W, ns)
+        assert all(torch.equal(a, b) for pair in got[s] for a, b in zip(pair, want))
+
+
+def test_steps_on_two_streams_at_once(cuda):
+    """Forward and backward of two problems, call by call on two streams, next to a plain kernel on a third."""
+    W, ns = 60, 4
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    probs = [(qkv(1, 1300, 4, 2, 64, seed=71), normal(74, 1, 1300, 4, 64)),
+             (qkv(2, 900, 3, 1, 128, seed=75), normal(78, 2, 900, 3, 128))]
+
+    def step(p, stream=None):
+        (q, k, v), do = p
+        out, lse = api.window_attn_fwd(q, k, v, W, ns, stream=stream)
+        return (out, lse, *api.window_attn_bwd(q, k, v, out, lse, do, W, ns, stream=stream))
+
+    want = [step(p) for p in probs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(25):
+        for s in (0, 1):
+            got[s].append(step(probs[s], streams[s]))
+        probs[0][1] + 1
+    torch.cuda.synchronize()
+    for s in (0, 1):
+        assert all(torch.equal(a, b) for r in got[s] for a, b in zip(r, want[s]))
 
 
 def test_decode_lens_outside_the_cache_are_clamped(cuda):

@@ -14,7 +14,7 @@ BAD_SHAPES = [
     (dict(B=0), INVALID), (dict(S=0), INVALID), (dict(Hq=-1), INVALID), (dict(Hkv=0), INVALID),
     (dict(window=0), INVALID), (dict(sinks=-1), INVALID), (dict(cu=FAKE, n_docs=0), INVALID),
     (dict(D=96), UNSUPPORTED), (dict(Hkv=3), UNSUPPORTED), (dict(sinks=129), UNSUPPORTED),
-    (dict(S=1 << 28, Hq=8), UNSUPPORTED),
+    (dict(S=1 << 28, Hq=8), UNSUPPORTED), (dict(S=(1 << 30) + 1, Hq=1, Hkv=1), UNSUPPORTED),
 ]
 
 
@@ -58,6 +58,8 @@ def test_workspace_sizes():
     assert ws(1, 100, 4, 2, 64, 100, 2, 0, 1) == 256 + tables            # nobody is far from a sink
     part, sums = 4 * 2 * 1 * 2 * 2 * 64, 4 * 2 * 3 * 2 * 2 * 64
     assert ws(1, 100, 4, 2, 64, 10, 2, 3, 1) == 256 + tables + part + sums
+    # short documents without end: no sums
+    assert ws(1, 100, 4, 2, 64, 10, 2, 5, 1) == ws(1, 100, 4, 2, 64, 10, 2, 100000, 1) == 256 + tables + part
     assert ws(1, 100, 4, 3, 64, 10, 2, 0, 1) == 0 and ws(1, 100, 4, 2, 64, 0, 2, 0, 0) == 0
     assert ws(1, 100, 4, 2, 64, 10, 2, -1, 0) == 0
     wd = B_.usp_window_decode_workspace_size
@@ -78,7 +80,7 @@ def decode(**kw):
     (dict(N=0), INVALID), (dict(n=0), INVALID), (dict(cap=0), INVALID), (dict(window=0), INVALID),
     (dict(sinks=-1), INVALID), (dict(D=80), UNSUPPORTED), (dict(Hq=5), UNSUPPORTED), (dict(n=17), UNSUPPORTED),
     (dict(sinks=129), UNSUPPORTED), (dict(ks=(12800, 132, 64)), INVALID), (dict(vs=(-8, 128, 64)), INVALID),
-    (dict(N=1 << 24, Hq=64), UNSUPPORTED),
+    (dict(N=1 << 24, Hq=64), UNSUPPORTED), (dict(cap=(1 << 30) + 1), UNSUPPORTED),
     # a long cache of one sequence: partials of the splits
     (dict(N=1, Hkv=1, cap=1 << 20, window=1 << 20, ws=None), WORKSPACE),
     (dict(N=1, Hkv=1, cap=1 << 20, window=1 << 20, nb=256), WORKSPACE),
@@ -122,6 +124,12 @@ JOB = (FAKE, FAKE, 2, (64, 32, 16), (64, 32, 16))
     (dict(jobs=[(None,) + JOB[1:]]), INVALID), (dict(jobs=[(FAKE, FAKE + 1) + JOB[2:]]), INVALID),
     (dict(jobs=[(FAKE, FAKE, 0) + JOB[3:]]), INVALID), (dict(jobs=[JOB[:3] + ((64, -32, 16), (64, 32, 16))]), INVALID),
     (dict(jobs=[JOB[:4] + ((64, 32, 0),)]), INVALID),   # the output's heads on top of one another
+    (dict(B=2, jobs=[JOB[:4] + ((32, 32, 16),)]), INVALID),              # its sequences' tokens
+    (dict(jobs=[JOB[:4] + ((128, 32, 48),)]), INVALID),                  # a head among the next token's
+    (dict(jobs=[JOB[:3] + ((64, 16, 32), (64, 32, 16))]), INVALID),      # in place with other strides
+    (dict(jobs=[JOB, JOB]), INVALID),                                    # the same tensor twice
+    (dict(jobs=[JOB, (FAKE, 2 * FAKE) + JOB[2:]]), INVALID),             # one reads what the other writes
+    (dict(jobs=[(2 * FAKE, FAKE) + JOB[2:], (3 * FAKE, 2 * FAKE) + JOB[2:]]), INVALID),
 ])
 def test_rope_is_refused(kw, code):
     assert rope(**kw) == code and B_.usp_last_error()
