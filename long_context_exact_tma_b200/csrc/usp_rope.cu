@@ -94,6 +94,12 @@ __device__ __forceinline__ void store(T* p, const Chunk<T, V>& c) {
     for (int x = 0; x < V; ++x) p[x] = c.e[x];
 }
 
+// The rotated pair, its products and sums spelled out: left to the compiler, the variants contract them
+// differently, and a row's result would depend on its alignment.
+__device__ __forceinline__ float2 turned(float x1, float x2, float c, float s) {
+  return make_float2(__fmaf_rn(x1, c, -__fmul_rn(x2, s)), __fmaf_rn(x2, c, __fmul_rn(x1, s)));
+}
+
 // kPaired: a chunk of kV elements holds kV / 2 whole pairs; else it is kV first
 // elements, whose partners lie R / 2 on.
 template <class T, int kV, bool kPaired>
@@ -181,18 +187,18 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       if constexpr (kPaired) {
 #pragma unroll
         for (int f = 0; f < kF; ++f) {
-          const float x1 = widen(v1.e[2 * f]), x2 = widen(v1.e[2 * f + 1]);
-          v1.e[2 * f] = narrow<T>(x1 * c[f] - x2 * s[f]);
-          v1.e[2 * f + 1] = narrow<T>(x2 * c[f] + x1 * s[f]);
+          const float2 y = turned(widen(v1.e[2 * f]), widen(v1.e[2 * f + 1]), c[f], s[f]);
+          v1.e[2 * f] = narrow<T>(y.x);
+          v1.e[2 * f + 1] = narrow<T>(y.y);
         }
         store<T, kW>(to, v1);
       } else {
         Chunk<T, kV>& v2 = x2s[y];
 #pragma unroll
         for (int f = 0; f < kF; ++f) {
-          const float x1 = widen(v1.e[f]), x2 = widen(v2.e[f]);
-          v1.e[f] = narrow<T>(x1 * c[f] - x2 * s[f]);
-          v2.e[f] = narrow<T>(x2 * c[f] + x1 * s[f]);
+          const float2 y = turned(widen(v1.e[f]), widen(v2.e[f]), c[f], s[f]);
+          v1.e[f] = narrow<T>(y.x);
+          v2.e[f] = narrow<T>(y.y);
         }
         store<T, kV>(to, v1);
         store<T, kV>(to + a.R / 2, v2);

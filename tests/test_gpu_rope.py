@@ -92,6 +92,20 @@ def test_views_in_place_and_broadcast(dtype, cuda):
     assert torch.equal(qkv[:, :, Hq + Hkv:], before[:, :, Hq + Hkv:])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("paired", [False, True])
+def test_alignment_does_not_change_the_result(paired, dtype, cuda):
+    B, S, H, D = 2, 700, 9, 64
+    x = torch.randn((B, S, H, D), device="cuda").to(dtype)
+    odd = torch.empty(x.numel() + 1, dtype=dtype, device="cuda")[1:].view(x.shape).copy_(x)
+    pos = torch.randint(-9, 10 ** 6, (2, B, S), device="cuda")
+    inv, axis = freqs(48, 2)
+    want = api.rope_axes(x, pos, inv, axis, paired=paired)
+    assert torch.equal(api.rope_axes(odd, pos, inv, axis, paired=paired), want)
+    assert torch.equal(api.rope_axes([odd, x], pos, inv, axis, paired=paired)[1], want)
+    assert torch.equal(api.rope_axes(x, pos, inv, axis, paired=paired, outs=x), want)
+
+
 def test_inverse_is_the_gradient_and_differences(cuda):
     """The gradient of sum(w * rope(x)) is rope(w, inverse): against 64-bit central differences."""
     B, S, H, D = 1, 9, 2, 32
