@@ -391,32 +391,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t cS = col_s(n & 1);
         const int k0 = kr.base(it), width = kr.width(it);
         const bool whole = k0 >= first_all && k0 + kBN - 1 <= x.q0;
-        const bool used = cbase < width;  // a narrow tile has the first 32 columns at most: warpgroup 0, half 0
-        // all of this thread's dP first, so that the next tile's dP can start while this one is worked on
-        uint32_t rp[2][32];
-        if (used) {
-          tmem_ld32(trow + kColDP + cbase, rp[0]);
-          if (width == kBN) tmem_ld32(trow + kColDP + cbase + 32, rp[1]);
-          tmem_ld_wait();
-          reg_fence32(rp[0]);
-          reg_fence32(rp[1]);
-        }
-        tc_fence_before();
-        mbar_arrive_warp(&bars->dp_free);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int c0 = cbase + half * 32;
-          if (c0 >= width) break;
-          uint32_t rs[32];
+        // (one copy of the code for both halves: the kernel's instructions stay in the cache)
+        const int c_end = min(cbase + 64, width);  // a narrow tile has the first 32 columns at most: warpgroup 0
+        if (cbase >= c_end) mbar_arrive_warp(&bars->dp_free);
+#pragma unroll 1
+        for (int c0 = cbase; c0 < c_end; c0 += 32) {
+          uint32_t rs[32], rp[32];
+          tmem_ld32(trow + kColDP + c0, rp);
           tmem_ld32(trow + cS + c0, rs);
           tmem_ld_wait();
+          reg_fence32(rp);
           reg_fence32(rs);
+          if (c0 + 32 >= c_end) {  // the tile's dP has been read: the next one's may start
+            tc_fence_before();
+            mbar_arrive_warp(&bars->dp_free);
+          }
           if (!whole) {
             // (a sink tile ends where the window tiles begin)
             const uint32_t vis = k0 < w0 ? bits_between(lo - k0, min(sink_end, w0) - k0, c0)
                                          : bits_between(first - k0, end - k0, c0) | bits_between(lo - k0, sink_end - k0, c0);
             hide_columns(rs, vis, kMinusInf);
-            hide_columns(rp[half], vis, 0u);  // columns past a narrow tile's width hold what an earlier tile left
+            // columns past a narrow tile's width hold what was there before (a hidden key's dP is finite: P = 0 hides it)
+            if (width != kBN) hide_columns(rp, vis, 0u);
           }
           uint32_t dk[16];
           if (it < kr.n1) {
@@ -425,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float2 y = ffma2(make_float2(__uint_as_float(rs[c]), __uint_as_float(rs[c + 1])), sl2, nl2);
               const float2 pv = make_float2(ex2_approx(y.x), ex2_approx(y.y));  // -inf -> 0
               const float2 ds =
-                  fmul2(pv, fadd2(make_float2(__uint_as_float(rp[half][c]), __uint_as_float(rp[half][c + 1])), nd2));
+                  fmul2(pv, fadd2(make_float2(__uint_as_float(rp[c]), __uint_as_float(rp[c + 1])), nd2));
               res2 = fadd2(res2, ds);
               dk[c >> 1] = pack_bf16x2(ds.x, ds.y);
             }
@@ -436,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               dk[c >> 1] = pack_bf16x2(fix * ex2_approx(y.x), fix * ex2_approx(y.y));
             }
           }
-          tmem_st16(trow + cS + cbase + half * 16, dk);
+          tmem_st16(trow + cS + cbase + (c0 - cbase) / 2, dk);
         }
         if (it + 1 == kr.n1) sRes[(item & 1) * 256 + wg * 128 + row] = res2.x + res2.y;
         tmem_st_wait();

@@ -52,8 +52,8 @@ struct FarCfg {
   static constexpr int kHalf = 16 * kRowBytes;
   static constexpr int kStageBytes = 2 * kHalf;  // a warp's 16 rows of Q, then of dO
   static constexpr int kWarpBytes = kStages * kStageBytes;
-  static constexpr int kOffSum = kWarps * kWarpBytes;  // fp32 [kGroup][2][D]
-  static constexpr int kSmemBytes = kOffSum + kGroup * 2 * D * 4;
+  static constexpr int kSmemBytes = kWarps * kWarpBytes;
+  static_assert(kGroup * 2 * D * 4 <= kWarpBytes, "a warp's sums fit over its buffers");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
@@ -70,7 +70,6 @@ __global__ void __launch_bounds__(kThreads, 1) far_kernel(const FarArgs a) {
   const int cx = blockIdx.x % a.n_chunks, gl = blockIdx.x / a.n_chunks % g.Hkv, b = blockIdx.x / a.n_chunks / g.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = smem_addr(smem), mine = base + warp * C::kWarpBytes;
-  float* sums = reinterpret_cast<float*>(smem + C::kOffSum);
   const int m_end = min((cx + 1) * a.chunk, g.n_tiles);
   let_next_start();
   wait_for_previous();
@@ -104,8 +103,6 @@ __global__ void __launch_bounds__(kThreads, 1) far_kernel(const FarArgs a) {
         cp_async_commit();
       };
       for (int st = 0; st < kStages - 1; ++st) fetch(st);
-      __syncthreads();  // the previous group's sums have been written out
-      for (int x = tid; x < kGroup * 2 * D; x += kThreads) sums[x] = 0.f;
       // B fragments of K and V: lane (g = lane/4, c = lane%4) holds elements 2c, 2c+1 and 2c+8, 2c+9 of
       // every 16 of sink g's row
       uint32_t kb[D / 16][2], vb[D / 16][2];
@@ -120,7 +117,6 @@ __global__ void __launch_bounds__(kThreads, 1) far_kernel(const FarArgs a) {
             vb[kk][y] = s < n_sinks ? *reinterpret_cast<const uint32_t*>(a.v + e + kk * 16 + y * 8) : 0u;
           }
       }
-      __syncthreads();
       // first far tile of this lane's two sink columns
       int far_from[2];
 #pragma unroll
@@ -186,22 +182,25 @@ __global__ void __launch_bounds__(kThreads, 1) far_kernel(const FarArgs a) {
         }
         __syncwarp();  // every lane has read the stage before it is filled again
       }
-      for (int y = 0; y < kWarps; ++y) {  // warp by warp: a fixed order of the sum
-        __syncthreads();
-        if (warp == y) {
+      // the warps' sums over their own buffers, then added warp by warp
+      float* mysum = reinterpret_cast<float*>(smem + warp * C::kWarpBytes);
 #pragma unroll
-          for (int x = 0; x < D / 16; ++x)
+      for (int x = 0; x < D / 16; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int s = (lane & 3) * 2 + (e & 1), d = x * 16 + (lane >> 2) + (e >> 1) * 8;
-              sums[(s * 2 + 0) * D + d] += ak[x][e];
-              sums[(s * 2 + 1) * D + d] += av[x][e];
-            }
+        for (int e = 0; e < 4; ++e) {
+          const int s = (lane & 3) * 2 + (e & 1), d = x * 16 + (lane >> 2) + (e >> 1) * 8;
+          mysum[(s * 2 + 0) * D + d] = ak[x][e];
+          mysum[(s * 2 + 1) * D + d] = av[x][e];
         }
-      }
       __syncthreads();
       const int n = min(kGroup, n_sinks - s0) * 2 * D;
-      for (int x = tid; x < n; x += kThreads) part[static_cast<size_t>(s0) * 2 * D + x] = sums[x];
+      for (int x = tid; x < n; x += kThreads) {
+        float t = 0.f;
+#pragma unroll
+        for (int y = 0; y < kWarps; ++y) t += reinterpret_cast<const float*>(smem + y * C::kWarpBytes)[x];
+        part[static_cast<size_t>(s0) * 2 * D + x] = t;
+      }
+      __syncthreads();  // read before the buffers are filled again
     }
   }
   cp_async_wait<0>();
