@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_sink = t_end > 0 ? kr.n_s : 0, n_end = n + n_sink + max(t_end - t_begin, 0);
       const float2 sl2 = make_float2(g.scale_log2, g.scale_log2);
       auto rescale_o = [&](float alpha) {  // the previous PV has landed: S_t is issued behind it
-#pragma unroll
+#pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t o[32];
           tmem_ld32(trow + cO + c0, o);
