@@ -95,42 +95,39 @@ struct Ring {
 };
 
 // ---------------------------------------------------------------- row stores
-// A warp's 32 rows of 32 bf16 columns, row = lane, 64 bytes of it in c: exchanged among
-// groups of four lanes so that lane 4a + k holds 16-byte piece k of rows 4a .. 4a + 3,
-// and a store instruction covers whole 64-byte runs of eight rows. (One row per lane
-// touches 32 cache lines per instruction; an item's stores then cost the CTA 2 us.)
-__device__ __forceinline__ void transpose_pieces(uint4 (&c)[4]) {
-  const int lane = threadIdx.x & 31;
-  auto swap = [&](uint4& keep0, uint4& keep1, int bit) {  // keep0 leaves lanes with the bit set, keep1 the others
-    const bool up = lane & bit;
-    uint4 out = up ? keep0 : keep1;
-    out.x = __shfl_xor_sync(0xffffffffu, out.x, bit);
-    out.y = __shfl_xor_sync(0xffffffffu, out.y, bit);
-    out.z = __shfl_xor_sync(0xffffffffu, out.z, bit);
-    out.w = __shfl_xor_sync(0xffffffffu, out.w, bit);
-    if (up)
-      keep0 = out;
-    else
-      keep1 = out;
-  };
-  swap(c[0], c[1], 1);
-  swap(c[2], c[3], 1);
-  swap(c[0], c[2], 2);
-  swap(c[1], c[3], 2);
-}
-// Row `row0 + lane` of the warp's 32 rows holds 32 columns from c0 on in pk (bf16 pairs); rows below
-// `rows` are stored at base + row * row_step.
+// A warp's 32 rows of 32 bf16 columns, row = lane, 64 bytes of it in pk: exchanged between
+// neighbouring lanes so that lane 2a + k holds 32-byte piece k of rows 2a and 2a + 1, and a
+// store instruction covers the whole 64-byte runs of sixteen rows. (One row per lane touches 32
+// cache lines with 16 bytes each; an item's stores then cost the CTA 2 us. Pieces of 16 bytes
+// among four lanes take twice the exchanges.) Rows below `rows` are stored at
+// base + row * row_step; an output that is only 16-byte aligned takes two stores for one.
 __device__ __forceinline__ void store_rows32(__nv_bfloat16* base, size_t row_step, int row0, int rows, int c0,
-                                             const uint32_t (&pk)[16]) {
-  uint4 c[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) c[q] = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
-  transpose_pieces(c);
+                                             uint32_t (&pk)[16]) {
   const int lane = threadIdx.x & 31;
+  const bool odd = lane & 1;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = row0 + (lane & ~3) + j;
-    if (r < rows) *reinterpret_cast<uint4*>(base + r * row_step + c0 + (lane & 3) * 8) = c[j];
+  for (int e = 0; e < 8; ++e) {  // even lanes give their second piece for the neighbour's first
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? pk[e] : pk[8 + e], 1);
+    if (odd)
+      pk[e] = got;
+    else
+      pk[8 + e] = got;
+  }
+  const bool whole = (reinterpret_cast<uintptr_t>(base) & 31u) == 0;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int r = row0 + (lane & ~1) + j;
+    if (r >= rows) break;
+    __nv_bfloat16* const p = base + r * row_step + c0 + (lane & 1) * 16;
+    const uint32_t* v = pk + 8 * j;
+    if (whole) {
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                   "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                   : "memory");
+    } else {
+      reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
   }
 }
 
