@@ -21,6 +21,7 @@
 #include <math.h>
 
 #include "../../include/usp.h"
+#include "usp_div.cuh"
 #include "usp_internal.h"
 #include "usp_ptx.cuh"
 
@@ -37,21 +38,6 @@ struct Job {
   int H, groups, g0;  // heads; threads that share a token's heads; the first of them
   long long s_b, s_t, s_h, d_b, d_t, d_h;
 };
-
-// n / d by a multiplication (n < 2^31): with m = 2^31 / d rounded up to 32 + shift bits, the
-// product's upper part is the quotient.
-struct Div {
-  uint32_t d, mul, shift;
-};
-Div make_div(uint32_t d) {
-  uint32_t shift = 0;
-  while ((1ull << shift) < d) ++shift;
-  const uint64_t m = ((1ull << (31 + shift)) + d - 1) / d;
-  return Div{d, static_cast<uint32_t>(m), shift};
-}
-__device__ __forceinline__ uint32_t quot(const Div& v, uint32_t n) {
-  return static_cast<uint32_t>((static_cast<uint64_t>(n) * v.mul) >> (31 + v.shift));
-}
 
 struct RopeArgs {
   Job job[USP_MAX_ROPE_JOBS];

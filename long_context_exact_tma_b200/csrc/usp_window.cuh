@@ -18,6 +18,7 @@
 #include <climits>
 
 #include "usp_attn_common.cuh"
+#include "usp_div.cuh"
 #include "usp_internal.h"
 #include "usp_ptx.cuh"
 
@@ -60,6 +61,19 @@ __device__ __forceinline__ KeyRun key_run(const WinGeo& g, int q0, int qe) {
   r.n_s = (r.sinks + kSinkTile - 1) / kSinkTile;
   r.nt = r.n_s + (qe - 1) / kBN + 1 - r.w0;
   return r;
+}
+
+// An item's number, taken apart: which of n heads (or pairs of heads) it is, of which batch, and the rest.
+struct ItemDiv {
+  Div heads, batch;
+};
+inline ItemDiv make_item_div(int n, int B) { return ItemDiv{make_div(n), make_div(B)}; }
+struct ItemParts {
+  int head, b, rest;
+};
+__device__ __forceinline__ ItemParts item_parts(const ItemDiv& d, int idx) {
+  const uint32_t x = quot(d.heads, idx), y = quot(d.batch, x);
+  return ItemParts{static_cast<int>(idx - x * d.heads.d), static_cast<int>(x - y * d.batch.d), static_cast<int>(y)};
 }
 
 // Words of the workspace header behind the status word: the kernels' item counters.

@@ -51,6 +51,7 @@ struct Cfg {
 
 struct Args {
   WinGeo g;
+  ItemDiv div;
   const float* lse2;
   const float* delta;
   int Lp;
@@ -84,13 +85,14 @@ struct Item {
   int b, gl, n;   // batch, kv head, key tile
   int n_m, steps; // query tiles n .. n + n_m - 1 of every head of the group
 };
-__device__ __forceinline__ Item item_of(const WinGeo& g, int idx) {
-  Item x;
+__device__ __forceinline__ Item item_of(const Args& a, int idx) {
+  const WinGeo& g = a.g;
   // the first keys of every head first (the causally heaviest), the heads side by side
-  x.gl = idx % g.Hkv;
-  idx /= g.Hkv;
-  x.b = idx % g.B;
-  x.n = idx / g.B;
+  const ItemParts p = item_parts(a.div, idx);
+  Item x;
+  x.gl = p.head;
+  x.b = p.b;
+  x.n = p.rest;
   x.n_m = last_qtile(g, x.n) - x.n + 1;
   x.steps = x.n_m * g.G;
   return x;
@@ -163,10 +165,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int idx = blockIdx.x, next = 0;
     for (int item = 1; ok && idx < a.n_items; ++item, idx = next) {
-      const Item x = item_of(g, idx);
-      for (int k = 0; k < x.steps; ++k) {
+      const Item x = item_of(a, idx);
+      for (int k = 0, m = 0, h = x.gl * g.G; k < x.steps; ++k) {  // m: query tile of head h
         const int s = issued % C::kStages;
-        const int h = x.gl * g.G + k / x.n_m, q0 = (x.n + k % x.n_m) * kBM;
+        const int q0 = (x.n + m) * kBM;
         if (issued >= C::kStages && !mbar_wait_w(&bars->qd_empty[s], ((issued / C::kStages) - 1) & 1, w, kSiteQdEmpty)) {
           ok = false;
           break;
@@ -180,6 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bulk_load_1d_w(sRow + s * 256, a.lse2 + rowbase, 512, &bars->qd_full[s]);
         bulk_load_1d_w(sRow + s * 256 + 128, a.delta + rowbase, 512, &bars->qd_full[s]);
         ++issued;
+        if (++m == x.n_m) m = 0, ++h;
         if (k == 0) {  // K, V behind the first Q, dO: their buffers free last
           if (n_kv >= 1 && !mbar_wait_w(&bars->kv_empty, (n_kv - 1) & 1, w, kSiteKvEmpty)) {
             ok = false;
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true, issued_any = false;
     int idx = blockIdx.x;
     if (idx < a.n_items) {
-      int steps = item_of(g, idx).steps, it = 0, item = 0;
+      int steps = item_of(a, idx).steps, it = 0, item = 0;
       ok = mbar_wait_w(&bars->kv_full, 0, w, kSiteKv) && mbar_wait_w(&bars->qd_full[0], 0, w, kSiteQd);
       if (ok) {
         tc_fence_after();
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool last = it + 1 == steps;
         if (last && !feed_take(bars->feed, item + 1, w, kSiteFeed, idx)) { ok = false; break; }
         const bool more = !last || idx < a.n_items;
-        const int next_steps = last && more ? item_of(g, idx).steps : steps;
+        const int next_steps = last && more ? item_of(a, idx).steps : steps;
         if (!mbar_wait_w(&bars->p_full, k & 1, w, kSiteP)) { ok = false; break; }
         tc_fence_after();
         issue_acc(kColDV, kColS, dDOmn, s, it == 0);  // dV += P^T dO
@@ -300,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int k = 0, idx = blockIdx.x;
     for (int item = 1; ok && idx < a.n_items; ++item) {
-      const Item x = item_of(g, idx);
+      const Item x = item_of(a, idx);
       const int k0 = x.n * kBN, j = k0 + row;
       const bool store = j < g.S;
       // queries that see the key: [j, q_end); none past the end of the sequence
@@ -314,9 +317,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int lo0, hi0;
       win_span(g, k0, lo0, hi0);
       const int q_all = min(hi0, k0 + g.W);
-      for (int it = 0; it < x.steps; ++it, ++k) {
+      for (int it = 0, m = 0; it < x.steps; ++it, ++k) {
         const int s = k % C::kStages;
-        const int q0 = (x.n + it % x.n_m) * kBM;
+        const int q0 = (x.n + m) * kBM;
+        if (++m == x.n_m) m = 0;
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->qd_full[s], (k / C::kStages) & 1, w, kSiteQdC));
         if (!ok) break;
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full, k & 1, w, kSiteS));
@@ -458,6 +462,7 @@ cudaError_t launch_d(const WinLaunch& L, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   Args a{};
   a.g = L.g;
+  a.div = make_item_div(L.g.Hkv, L.g.B);
   a.lse2 = L.lse2;
   a.delta = L.delta;
   a.Lp = L.Lp;

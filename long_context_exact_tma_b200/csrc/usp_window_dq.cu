@@ -58,6 +58,7 @@ struct Cfg {
 
 struct Args {
   WinGeo g;
+  ItemDiv div;
   const float* lse2;
   float* delta;
   int Lp;
@@ -90,14 +91,10 @@ enum : int {
 struct Item {
   int b, h, q0;
 };
-__device__ __forceinline__ Item item_of(const WinGeo& g, int idx) {
-  Item x;
+__device__ __forceinline__ Item item_of(const Args& a, int idx) {
   // as in the forward: the last rows of every head first, the heads side by side
-  x.h = idx % g.Hq;
-  idx /= g.Hq;
-  x.b = idx % g.B;
-  x.q0 = (g.n_tiles - 1 - idx / g.B) * kBM;
-  return x;
+  const ItemParts p = item_parts(a.div, idx);
+  return Item{p.b, p.head, (a.g.n_tiles - 1 - p.rest) * kBM};
 }
 // The item's key tiles, n1 of them, and for its rows of few keys the last n2 again
 // (such a row's keys end at the diagonal; nt in all).
@@ -199,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int idx = blockIdx.x, next = 0;
     for (int k = 1; ok && idx < a.n_items; ++k, idx = next) {
-      const Item x = item_of(g, idx);
+      const Item x = item_of(a, idx);
       const DqRun kr = run_of(g, x);
       const int kvh = x.h / g.G;
       for (int it = 0; it < kr.nt; ++it) {
@@ -308,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int idx = blockIdx.x;
     DqRun r{};
     if (idx < a.n_items) {
-      r = run_of(g, item_of(g, idx));
+      r = run_of(g, item_of(a, idx));
       ok = mbar_wait_w(&bars->q_full, 0, w, kSiteQ) && issue_s(r.width(0));
       if (ok && r.nt == 1) umma_commit_w(&bars->q_empty);
       ok = ok && mbar_wait_w(&bars->do_full, 0, w, kSiteDo) && issue_dp(r.width(0));
@@ -337,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++item;
       if (!ok || !(ok = feed_take(bars->feed, item, w, kSiteFeed, idx)) || idx >= a.n_items) break;
       // the next item's first tile, behind this one's last dQ: its Q and dO may still be on their way
-      r = run_of(g, item_of(g, idx));
+      r = run_of(g, item_of(a, idx));
       ok = mbar_wait_w(&bars->q_full, item & 1, w, kSiteQ) && issue_s(r.width(0));
       if (ok && r.nt == 1) umma_commit_w(&bars->q_empty);
       ok = ok && mbar_wait_w(&bars->do_full, item & 1, w, kSiteDo) && issue_dp(r.width(0));
@@ -359,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int n = 0, item = 0, idx = blockIdx.x;
     for (; ok && idx < a.n_items; ++item) {
-      const Item x = item_of(g, idx);
+      const Item x = item_of(a, idx);
       const DqRun kr = run_of(g, x);
       const int i = x.q0 + row;
       const bool store = i < g.S;
@@ -484,6 +481,7 @@ cudaError_t launch_d(const WinLaunch& L, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   Args a{};
   a.g = L.g;
+  a.div = make_item_div(L.g.Hq, L.g.B);
   a.lse2 = L.lse2;
   a.delta = L.delta;
   a.Lp = L.Lp;

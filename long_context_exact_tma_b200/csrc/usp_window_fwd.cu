@@ -57,6 +57,7 @@ struct Cfg {
 
 struct Args {
   WinGeo g;
+  ItemDiv div;
   __nv_bfloat16* out;
   float* lse;
   int n_items;
@@ -89,14 +90,13 @@ struct Item {
 // The last rows of every head come first, the heads of a batch side by side: their
 // key tiles are in L2 for the rows before them, and the short walks of the first rows
 // fill the end of the launch.
-__device__ __forceinline__ Item item_of(const WinGeo& g, int idx) {
+__device__ __forceinline__ Item item_of(const Args& a, int idx) {
+  const WinGeo& g = a.g;
   Item x;
   const int n_m = g.pair_heads ? g.n_tiles : (g.n_tiles + 1) / 2;
-  const int n_u = g.pair_heads ? g.Hq / 2 : g.Hq;
-  const int u = idx % n_u;
-  idx /= n_u;
-  x.b = idx % g.B;
-  const int m = n_m - 1 - idx / g.B;
+  const ItemParts p = item_parts(a.div, idx);
+  const int u = p.head, m = n_m - 1 - p.rest;
+  x.b = p.b;
   if (g.pair_heads) {
     x.h = 2 * u;
     x.q0 = m * kBM;
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int idx = blockIdx.x, next = 0;
     for (int k = 1; ok && idx < a.n_items; ++k, idx = next) {
-      const Item x = item_of(g, idx);
+      const Item x = item_of(a, idx);
       const KeyRun kr = key_run(g, x.q0, x.q_end(g));
       for (int it = 0; it < kr.nt; ++it) {
         const int s = issued % n_st;
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t item = 0;
     int idx = blockIdx.x;
     while (ok && idx < a.n_items) {
-      const ItemRun r = run_of(g, item_of(g, idx));
+      const ItemRun r = run_of(g, item_of(a, idx));
       const int nt = r.kr.nt;
       // the item's first S, behind the last PV of the item before
       ok = mbar_wait_w(&bars->q_full, item & 1, w, kSiteQ) && mbar_wait_w(&bars->k_full[k_s.at], k_s.phase, w, kSiteK);
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int n = 0;  // key tile of the CTA's stream
     int idx = blockIdx.x;
     for (int k = 1; ok && idx < a.n_items; ++k) {
-      const Item x = item_of(g, idx);
+      const Item x = item_of(a, idx);
       const ItemRun r = run_of(g, x);
       const KeyRun& kr = r.kr;
       const int h = x.h + t * x.dh, q0 = x.q0 + t * x.dq;
@@ -560,6 +560,7 @@ cudaError_t launch_d(const WinLaunch& L, cudaStream_t stream) {
   Args a{};
   a.g = L.g;
   a.g.pair_heads = kHeads;
+  a.div = make_item_div(kHeads ? L.g.Hq / 2 : L.g.Hq, L.g.B);
   a.out = static_cast<__nv_bfloat16*>(L.out);
   a.lse = L.lse;
   a.status = L.status;
