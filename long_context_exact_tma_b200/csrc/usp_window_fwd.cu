@@ -7,7 +7,9 @@
 // A persistent CTA (one per SM, 352 threads) takes work items: two 128-row query
 // tiles that share every key tile -- the same rows of two heads of a group when
 // the group is even (then both tiles need exactly the same keys), else two
-// consecutive row tiles of a head, each taking the key tiles of its own window. Roles:
+// consecutive row tiles of a head, each taking the key tiles of its own window. Items of
+// one query tile take 55 to 65 % of a pair's time; the pairs that would leave half of the
+// SMs idle at the end of the launch are taken apart into them. Roles:
 //   warp 0      TMA producer of K (3 stages) and of the item's two Q tiles
 //   warp 10     TMA producer of V
 //   warp 1      UMMA issuer: per key tile and query tile t, O_t += P_t V (A = P_t
@@ -58,6 +60,7 @@ struct Cfg {
 struct Args {
   WinGeo g;
   ItemDiv div;
+  int n_pairs;  // the items from here on are single query tiles; 0: all, numbered by head
   __nv_bfloat16* out;
   float* lse;
   int n_items;
@@ -84,6 +87,7 @@ enum : int {
 struct Item {
   int b, h, q0;     // batch, head and first row of query tile 0
   int dh, dq;       // what tile 1 adds to them
+  bool one;         // there is no tile 1
   __device__ __forceinline__ int q_end(const WinGeo& g) const { return min(q0 + dq + kBM, g.S); }
 };
 
@@ -93,20 +97,23 @@ struct Item {
 __device__ __forceinline__ Item item_of(const Args& a, int idx) {
   const WinGeo& g = a.g;
   Item x;
-  const int n_m = g.pair_heads ? g.n_tiles : (g.n_tiles + 1) / 2;
+  x.dh = x.dq = 0;
+  x.one = idx >= a.n_pairs;
+  const int half = x.one && a.n_pairs > 0 ? (idx - a.n_pairs) & 1 : 0;
+  if (x.one && a.n_pairs > 0) idx = a.n_pairs + ((idx - a.n_pairs) >> 1);
   const ItemParts p = item_parts(a.div, idx);
-  const int u = p.head, m = n_m - 1 - p.rest;
   x.b = p.b;
-  if (g.pair_heads) {
-    x.h = 2 * u;
-    x.q0 = m * kBM;
-    x.dh = 1;
-    x.dq = 0;
+  if (a.n_pairs == 0) {
+    x.h = p.head;
+    x.q0 = (g.n_tiles - 1 - p.rest) * kBM;
+  } else if (g.pair_heads) {
+    x.h = 2 * p.head + half;
+    x.q0 = (g.n_tiles - 1 - p.rest) * kBM;
+    x.dh = x.one ? 0 : 1;
   } else {
-    x.h = u;
-    x.q0 = 2 * m * kBM;
-    x.dh = 0;
-    x.dq = kBM;
+    x.h = p.head;
+    x.q0 = (2 * ((g.n_tiles + 1) / 2 - 1 - p.rest) + half) * kBM;
+    x.dq = x.one ? 0 : kBM;
   }
   return x;
 }
@@ -138,10 +145,11 @@ __device__ __forceinline__ ItemRun run_of(const WinGeo& g, const Item& x) {
       r.end1 = 0;
     }
   }
+  if (x.one) r.end1 = 0;
   return r;
 }
 
-// kHeads: the items' tiles are two heads of a group (both take every key tile).
+// kHeads: the pairs are two heads of a group (both tiles take every key tile).
 template <int D, bool kHeads>
 __global__ void __launch_bounds__(kThreads, 1)
     window_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -227,8 +235,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          mbar_expect_tx_w(&bars->q_full, 2 * C::kTileBytes);
-          for (int t = 0; t < 2; ++t)
+          const int n_t = x.one ? 1 : 2;
+          mbar_expect_tx_w(&bars->q_full, n_t * C::kTileBytes);
+          for (int t = 0; t < n_t; ++t)
             for (int p = 0; p < C::kPanels; ++p)
               tma_load_4d_w(&tm_q, &bars->q_full, sQ + t * C::kTileBytes + p * C::kPanelBytes, p * 64, x.h + t * x.dh,
                             x.q0 + t * x.dq, x.b);
@@ -309,10 +318,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && idx < a.n_items) {
       const ItemRun r = run_of(g, item_of(a, idx));
       const int nt = r.kr.nt;
+      auto takes = [&](int t, int it) { return kHeads ? t == 0 || r.end1 > 0 : r.takes(t, it); };
       // the item's first S, behind the last PV of the item before
       ok = mbar_wait_w(&bars->q_full, item & 1, w, kSiteQ) && mbar_wait_w(&bars->k_full[k_s.at], k_s.phase, w, kSiteK);
       for (int t = 0; ok && t < 2; ++t)
-        if (kHeads || r.takes(t, 0)) ok = issue_s(t, r.kr.width(0));
+        if (takes(t, 0)) ok = issue_s(t, r.kr.width(0));
       if (!ok) break;
       umma_commit_w(&bars->k_empty[k_s.at]);
       k_s.next();
@@ -324,14 +334,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         // while the other's softmax works
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if ((kHeads || r.takes(t, it)) && !issue_pv(t, r.kr.width(it), kHeads || t == 0 || r.kr.n_s > 0 ? it == 0 : it == r.begin1)) {
+          if (takes(t, it) && !issue_pv(t, r.kr.width(it), kHeads || t == 0 || r.kr.n_s > 0 ? it == 0 : it == r.begin1)) {
             ok = false;
             break;
           }
           if (t == 1) umma_commit_w(&bars->v_empty[v_p.at]);
           if (more) {
             if (t == 0 && !mbar_wait_w(&bars->k_full[k_s.at], k_s.phase, w, kSiteK)) { ok = false; break; }
-            if ((kHeads || r.takes(t, it + 1)) && !issue_s(t, r.kr.width(it + 1))) { ok = false; break; }
+            if (takes(t, it + 1) && !issue_s(t, r.kr.width(it + 1))) { ok = false; break; }
             if (t == 1) {
               umma_commit_w(&bars->k_empty[k_s.at]);
               if (it + 2 == nt) umma_commit_w(&bars->q_empty);
@@ -377,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_use = -INFINITY, l_run = 0.f, lb_run = 0.f;
       const int n0 = n;
       // this tile's window tiles, from k0 on, behind the sinks'
-      const int t_begin = kHeads || t == 0 ? kr.n_s : r.begin1, t_end = kHeads ? kr.nt : t == 0 ? r.end0 : r.end1;
+      const int t_begin = kHeads || t == 0 ? kr.n_s : r.begin1, t_end = t == 0 ? r.end0 : r.end1;
       const int n_sink = t_end > 0 ? kr.n_s : 0, n_end = n + n_sink + max(t_end - t_begin, 0);
       const float2 sl2 = make_float2(g.scale_log2, g.scale_log2);
       auto rescale_o = [&](float alpha) {  // the previous PV has landed: S_t is issued behind it
@@ -560,16 +570,29 @@ cudaError_t launch_d(const WinLaunch& L, cudaStream_t stream) {
   Args a{};
   a.g = L.g;
   a.g.pair_heads = kHeads;
-  a.div = make_item_div(kHeads ? L.g.Hq / 2 : L.g.Hq, L.g.B);
   a.out = static_cast<__nv_bfloat16*>(L.out);
   a.lse = L.lse;
   a.status = L.status;
   a.wait_ns = L.wait_ns;
-  const long long items = a.g.pair_heads ? static_cast<long long>(L.g.n_tiles) * (L.g.Hq / 2) * L.g.B
-                                         : static_cast<long long>((L.g.n_tiles + 1) / 2) * L.g.Hq * L.g.B;
-  if (items > 0x3FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  a.n_items = static_cast<int>(items);
+  const int heads = kHeads ? L.g.Hq / 2 : L.g.Hq, rows = kHeads ? L.g.n_tiles : (L.g.n_tiles + 1) / 2;
+  const long long pairs = static_cast<long long>(rows) * heads * L.g.B;
+  if (pairs > 0x1FFFFFFFLL) return cudaErrorInvalidConfiguration;
+  // What the SMs' last round would take of the pairs, if it is no more than half a round, as single
+  // tiles (512 head pairs on 148 SMs, 2 or 3 key tiles each: 36.9 -> 35.4 us). The last row pair of a head may lack its
+  // second tile: it comes first, and is not taken apart.
   const int sms = sm_count();
+  const long long rest = pairs % sms;
+  a.n_pairs = static_cast<int>(pairs);
+  long long items = pairs;
+  if (pairs == rest && 2 * rest <= sms) {
+    a.n_pairs = 0;
+    items = static_cast<long long>(L.g.n_tiles) * L.g.Hq * L.g.B;
+  } else if (2 * rest <= sms && (kHeads || L.g.n_tiles % 2 == 0 || rest <= pairs - static_cast<long long>(heads) * L.g.B)) {
+    a.n_pairs = static_cast<int>(pairs - rest);
+    items = pairs + rest;
+  }
+  a.div = make_item_div(a.n_pairs ? heads : L.g.Hq, L.g.B);
+  a.n_items = static_cast<int>(items);
   const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);
   window_fwd_kernel<D, kHeads><<<grid, kThreads, C::kSmemBytes, stream>>>(L.tm_q, L.tm_k, L.tm_v, a);
   note_launch();

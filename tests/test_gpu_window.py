@@ -43,6 +43,8 @@ CASES = [
     (1, 500, 2, 2, 64, 1, 100, [0, 88, 500]),                    # two sink tiles of rows of few keys
     (2, 777, 3, 1, 128, 300, 70, [0, 500, 777]),                 # row pairs whose second tile starts behind the sinks
     (1, 650, 1, 1, 64, 140, 5, [0, 129, 300, 650]),
+    (1, 2600, 16, 16, 64, 70, 4, [0, 300, 1111, 2600]),          # more work items than SMs: a few left over,
+    (2, 1350, 16, 4, 64, 200, 2, None),                          # of row pairs and of head pairs
     (1, 2500, 1, 1, 64, 90, 6, [0] + list(range(60, 560, 5)) + [2300, 2500]),   # a long document among many short ones
 ]
 
@@ -166,6 +168,23 @@ def test_outputs_stay_inside_their_rows(cuda):
     for buf in [bo, bl] + [g[0] for g in grads]:
         m = buf.numel() - 4096
         assert (buf[:2048] == 7).all() and (buf[2048 + m:] == 7).all()
+
+
+def test_outputs_aligned_to_16_bytes(cuda):
+    """Outputs that start 16 bytes into a line, beside ones at its start: the same values."""
+    B, S, H, D, W, ns = 1, 300, 2, 128, 40, 2
+    q, k, v = qkv(B, S, H, H, D, seed=35)
+    do = normal(38, B, S, H, D)
+    want = api.window_attn_fwd(q, k, v, W, ns)
+    wg = api.window_attn_bwd(q, k, v, *want, do, W, ns)
+
+    def shifted(x):
+        return torch.empty(x.numel() + 8, dtype=x.dtype, device="cuda")[8:].view(x.shape)
+
+    out, lse = api.window_attn_fwd(q, k, v, W, ns, out=shifted(want[0]))
+    got = api.window_attn_bwd(q, k, v, out, lse, do, W, ns, dq=shifted(q), dk=shifted(k), dv=shifted(v))
+    assert all(x.data_ptr() % 32 == 16 for x in (out, *got))
+    assert all(torch.equal(a, b) for a, b in zip((out, lse, *got), (*want, *wg)))
 
 
 def test_other_stream_and_graph(cuda):
