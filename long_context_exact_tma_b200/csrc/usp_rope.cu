@@ -12,7 +12,7 @@
 // upper 32 bits, as a signed number, are the angle within half a turn.
 //
 // Bound by memory: each element is read and written once. A thread takes one
-// 16-byte chunk column (two in the halves form) of one token and walks some of its
+// 16-byte chunk column (two in the halves form, of the copied rest too) of one token and walks some of its
 // heads, four at a time, so that the sines are computed once per walk; the lanes of a warp cover
 // neighbouring chunks and heads. Views whose rows are not 16-byte aligned take the
 // same kernel with one-element chunks.
@@ -118,7 +118,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   const bool rot = chunk < n_rot;
   if (!rot && src == dst && job.s_h == job.d_h) return;
   const int e1 = rot ? static_cast<int>(chunk) * kW : a.R + static_cast<int>(chunk - n_rot) * kV;
-  const int e2 = e1 + a.R / 2;  // the halves form's partner
+  // the halves form's partner; of a copied chunk the one half of the rest on, if there is one (as many
+  // bytes as a rotated column: with one chunk each, half of each row rotated took 72 us against 55)
+  const int gap = rot ? a.R / 2 : static_cast<int>(a.chunks.d - n_rot) * kV;
+  const bool two = rot || e1 + gap < a.D;
   // the first heads' chunks are on their way while the sines are made
   constexpr int kAhead = 4;
   Chunk<T, kW> x1s[kAhead], x2s[kPaired ? 1 : kAhead];
@@ -135,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       else  // one element past R
         x1s[y].e[0] = p[0];
       if constexpr (!kPaired)
-        if (rot) x2s[y] = load<T, kV>(src + hy * job.s_h + e2);
+        if (two) x2s[y] = load<T, kV>(p + gap);
     }
   };
   fetch(h0);
@@ -168,6 +171,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
           store<T, kW>(to, v1);
         else
           to[0] = v1.e[0];
+        if constexpr (!kPaired)
+          if (two) store<T, kV>(to + gap, x2s[y]);
         continue;
       }
       if constexpr (kPaired) {
@@ -187,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
           v2.e[f] = narrow<T>(y.y);
         }
         store<T, kV>(to, v1);
-        store<T, kV>(to + a.R / 2, v2);
+        store<T, kV>(to + gap, v2);
       }
     }
   }
@@ -196,7 +201,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 template <class T, int kV, bool kPaired>
 cudaError_t launch(RopeArgs& a, long long tokens, cudaStream_t st) {
   constexpr int kF = kPaired ? (kV + 1) / 2 : kV;
-  const uint32_t n_chunks = a.R / 2 / kF + (a.D - a.R) / kV;
+  const uint32_t n_copy = (a.D - a.R) / kV;
+  const uint32_t n_chunks = a.R / 2 / kF + (kPaired ? n_copy : (n_copy + 1) / 2);
   // Heads per thread: as many as pay the sines back, fewer while the tokens alone do not fill the machine.
   int per = kHeadsPerThread;
   auto groups_at = [&](int hp) {
