@@ -236,7 +236,7 @@ struct WinLaunch {
   // [B][Hkv][run's first tile][ns][2][D]; null without such queries
   float* far_part;
   int far_chunk;
-  float* far_sum;  // their sums [B][Hkv][n_docs][ns][2][D], or null: few runs
+  float* far_sum;  // their sums [B][Hkv][n_docs][ns][2][D], or null: the items add the runs up
   int* status;
   unsigned long long wait_ns;
 };
@@ -248,7 +248,7 @@ cudaError_t launch_window_dq(const WinLaunch& L, cudaStream_t stream);
 cudaError_t launch_window_dkdv(const WinLaunch& L, cudaStream_t stream);
 int window_far_chunk(const WinGeo& g);
 bool window_far_summable(const WinGeo& g);
-bool window_far_summed(const WinGeo& g);
+bool window_far_summed(const WinGeo& g, int D);
 cudaError_t launch_window_far(const WinLaunch& L, cudaStream_t stream);
 
 // The current device's multiprocessor count.

@@ -131,7 +131,7 @@ extern "C" int usp_window_attn_bwd(const void* q, const void* k, const void* v, 
   if (has_far(L.g)) {
     L.far_part = delta + table_floats(L.g);
     L.far_chunk = window_far_chunk(L.g);
-    if (window_far_summed(L.g)) L.far_sum = L.far_part + far_part_floats(L.g, D);
+    if (window_far_summed(L.g, D)) L.far_sum = L.far_part + far_part_floats(L.g, D);
   }
   L.status = static_cast<int*>(workspace);
   L.wait_ns = current_wait_ns();

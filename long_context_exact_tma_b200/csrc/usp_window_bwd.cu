@@ -4,7 +4,7 @@
 //   P_ij = exp(scale q_i.k_j - LSE_i), dP = dO V^T, dS = P (dP - Delta),
 //   dK = scale dS^T Q, dV = P^T dO, summed over the query heads of a group,
 // over the query tiles in the band of each key tile (usp_window.cuh). Rows of
-// sinks add the sums that the far kernel made of the queries behind that band.
+// sinks add what the far kernel made of the queries behind that band.
 //
 // A persistent CTA (one per SM, 320 threads) takes work items: one 128-key tile
 // of one kv head, walked by steps (query head of the group, query tile):
@@ -57,7 +57,7 @@ struct Args {
   int Lp;
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
-  const float* far_part;  // see WinLaunch
+  float* far_part;  // see WinLaunch
   int far_chunk;
   const float* far_sum;
   int n_items;
@@ -69,6 +69,7 @@ struct Bars {
   uint64_t kv_full, kv_empty;
   uint64_t qd_full[2], qd_empty[2];
   uint64_t s_full, dp_full, p_full, ds_full, p_used, ds_used, drain;
+  uint64_t far_full;  // the runs of the item's far sinks have been added up
   ItemFeed feed;
   uint32_t tmem_base;
   int abort_flag;
@@ -77,6 +78,7 @@ struct Bars {
 enum : int {
   kSiteKvEmpty = 0x501, kSiteQdEmpty = 0x502, kSiteKv = 0x511, kSiteQd = 0x512, kSiteP = 0x513, kSitePUsed = 0x514,
   kSiteDs = 0x515, kSiteDsUsed = 0x516, kSiteS = 0x521, kSiteDp = 0x522, kSiteQdC = 0x523, kSiteEpi = 0x524,
+  kSiteFar = 0x525,
   kSiteFeed = 0x531,
   kSiteAlign = 0x5FF
 };
@@ -131,6 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars->dp_full, 1);
     mbar_init(&bars->p_full, kComputeWarps);
     mbar_init(&bars->ds_full, kComputeWarps);
+    mbar_init(&bars->far_full, kComputeWarps);
     mbar_init(&bars->p_used, 1);
     mbar_init(&bars->ds_used, 1);
     mbar_init(&bars->drain, 1);
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cbase = wg * 64;
     const float2 sl2 = make_float2(g.scale_log2, g.scale_log2);
     bool ok = true;
-    int k = 0, idx = blockIdx.x;
+    int k = 0, idx = blockIdx.x, n_far = 0;
     for (int item = 1; ok && idx < a.n_items; ++item) {
       const Item x = item_of(a, idx);
       const int k0 = x.n * kBN, j = k0 + row;
@@ -317,6 +320,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       int lo0, hi0;
       win_span(g, k0, lo0, hi0);
       const int q_all = min(hi0, k0 + g.W);
+      // The far queries' part of the sinks' gradients: of the document of the tile's last key (any other
+      // ends inside the tile), by runs f0 .. f1 whose first tiles are multiples of the chunk or the
+      // document's first tile, from the first query tile outside the key tile's band on. The runs are added
+      // up, over the first one, while the item's first tiles are on their way.
+      const float* far = nullptr;
+      bool far_wait = false;
+      if (a.far_part) {
+        const int jl = min(k0 + kBN, g.S) - 1;
+        int lol, hil;
+        win_span(g, jl, lol, hil);
+        const int mf = x.n + x.n_m, me = (hil - 1) / kBM + 1, s0 = max(k0 - lol, 0), s1 = min(g.ns, jl + 1 - lol);
+        if (mf < me && s0 < s1) {
+          const size_t bh = static_cast<size_t>(x.b) * g.Hkv + x.gl, run = static_cast<size_t>(g.ns) * (2 * D);
+          if (a.far_sum) {
+            const int d = g.cu ? doc_of(g.cu, g.n_docs, jl) : 0;
+            far = a.far_sum + (bh * g.n_docs + d) * run;
+          } else {
+            const int f0 = mf / a.far_chunk, f1 = (me - 1) / a.far_chunk, md = (lol + kBM - 1) / kBM;
+            float* const base = a.far_part + bh * g.n_tiles * run;
+            float* const sum = base + max(f0 * a.far_chunk, md) * run;
+            far = sum;
+            for (int u = s0 * (2 * D) + (threadIdx.x - 64) * 4; u < s1 * (2 * D); u += 32 * kComputeWarps * 4) {
+              float4 t = *reinterpret_cast<const float4*>(sum + u);
+#pragma unroll 8
+              for (int y = f0 + 1; y <= f1; ++y) {
+                const float4 p = *reinterpret_cast<const float4*>(base + y * a.far_chunk * run + u);
+                t.x += p.x;
+                t.y += p.y;
+                t.z += p.z;
+                t.w += p.w;
+              }
+              *reinterpret_cast<float4*>(sum + u) = t;
+            }
+            mbar_arrive_warp(&bars->far_full);
+            far_wait = true;
+          }
+        }
+      }
       for (int it = 0, m = 0; it < x.steps; ++it, ++k) {
         const int s = k % C::kStages;
         const int q0 = (x.n + m) * kBM;
@@ -386,30 +427,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ------------------------------------------------------------ dK, dV epilogue
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->ds_used, (k - 1) & 1, w, kSiteEpi));
+      if (ok && far_wait) ok = __all_sync(0xffffffffu, mbar_wait(&bars->far_full, n_far++ & 1, w, kSiteFar));
       if (ok) {
         tc_fence_after();
         const size_t kv0 = (static_cast<size_t>(x.b) * g.S * g.Hkv + x.gl) * D;  // row 0 of the kv head
-        // the far queries' part of a sink's gradients, dK then dV: their sum, or the partials of the runs f0 .. f1,
-        // whose first tiles are multiples of the chunk or the document's first tile, from the first query tile
-        // outside the key tile's band on
-        const float* far = nullptr;
-        int f0 = 0, f1 = -1, md = 0;
-        if (sink >= 0 && a.far_part) {
-          const int mf = x.n + x.n_m, me = (hi - 1) / kBM + 1;
-          if (mf < me) {
-            const size_t bh = static_cast<size_t>(x.b) * g.Hkv + x.gl;
-            if (a.far_sum) {
-              const int d = g.cu ? doc_of(g.cu, g.n_docs, j) : 0;
-              far = a.far_sum + ((bh * g.n_docs + d) * g.ns + sink) * (2 * D);
-              f1 = 0;
-            } else {
-              far = a.far_part + (bh * g.n_tiles * g.ns + sink) * (2 * D);
-              f0 = mf / a.far_chunk;
-              f1 = (me - 1) / a.far_chunk;
-              md = (lo + kBM - 1) / kBM;
-            }
-          }
-        }
+        // a row of far sinks: dK, then dV (a document that ends inside the tile has none)
+        const bool add = far && sink >= 0 && hi > (x.n + x.n_m) * kBM;
+        if (add) far += static_cast<size_t>(sink) * (2 * D);
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {  // dK, then dV
           const uint32_t col = half == 0 ? kColDK : kColDV;
@@ -421,9 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(trow + col + c0, r);
             tmem_ld_wait();
             reg_fence32(r);
-            for (int y = f0; y <= f1; ++y) {
-              const float4* p = reinterpret_cast<const float4*>(
-                  far + static_cast<size_t>(max(y * a.far_chunk, md)) * g.ns * (2 * D) + half * D + c0);
+            if (add) {
+              const float4* p = reinterpret_cast<const float4*>(far + half * D + c0);
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
                 const float4 f4 = p[c];

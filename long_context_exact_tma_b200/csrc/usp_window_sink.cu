@@ -33,6 +33,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = 8;   // sinks at a time
 constexpr int kStages = 3;  // (tile, head) steps in flight
+constexpr long long kFarOwn = 1 << 16;  // floats of runs that the key-major kernel adds up itself
 
 struct FarArgs {
   WinGeo g;
@@ -278,14 +279,15 @@ int window_far_chunk(const WinGeo& g) {
   return per_head > 1 ? static_cast<int>((g.n_tiles + per_head - 1) / per_head) : g.n_tiles;
 }
 
-// Up to 8 runs the epilogue of the few key tiles with sinks adds them itself (a training step on 515
-// tokens: 48 us against 51 with the second kernel); 32 runs there cost it more than a launch (a step on
-// 8192: 291 us against 283). Documents of less than 32 tokens on average: few of them reach past their
-// tile's band, and the sums would make most of the workspace; the epilogue adds there too.
+// Documents of less than 32 tokens on average: few of them reach past their tile's band, and the sums
+// would make most of the workspace.
 bool window_far_summable(const WinGeo& g) { return g.n_docs <= 4LL * g.n_tiles; }
-bool window_far_summed(const WinGeo& g) {
-  const int chunk = window_far_chunk(g);
-  return window_far_summable(g) && (g.n_tiles + chunk - 1) / chunk > 8;
+// Up to 256 KB of runs for a (document, kv head) the key-major kernel's items add them up themselves (the
+// backward of 8192 tokens, 16/4 heads, window 128: 133 us against 136 with a launch for 128 KB of runs;
+// window 512: 200 against 202 for 128 KB, but 231 against 221 for 544 KB).
+bool window_far_summed(const WinGeo& g, int D) {
+  const long long chunk = window_far_chunk(g), runs = (g.n_tiles + chunk - 1) / chunk;
+  return window_far_summable(g) && runs * g.ns * 2 * D > kFarOwn;
 }
 
 cudaError_t launch_window_far(const WinLaunch& L, cudaStream_t stream) {
