@@ -8,12 +8,15 @@
 //
 // A few keys against every query is bound by reading Q and dO once, so the
 // products run on the warp-level 16x8x16 matrix instruction (a 128-key tensor tile
-// would hold 4 keys in 128): warp = 16 query rows, 8 sinks at a time, the sinks
-// always the instruction's 8 columns: S [rows x sinks] and dP with K, V fragments
-// that stay in registers, then dV^T and dK^T [D x sinks]. A CTA takes
-// a run of query tiles of one document and kv head and streams its rows, tile by
-// tile and head by head; every warp fetches its own rows through its own ring of
-// cp.async buffers, so the loop has no block barrier. The warps' fp32 sums are
+// would hold 4 keys in 128): a warp has 8 sinks, always the instruction's 8 columns:
+// S [rows x sinks] and dP with K, V fragments that stay in registers, then dV^T and
+// dK^T [D x sinks], over 16 query rows at a time. A CTA takes a run of query tiles of
+// one document and kv head and streams its rows, tile by tile and head by head; every
+// warp fetches 16 of a tile's rows through its own ring of cp.async buffers. With up
+// to 8 sinks it also works on just these; with more, two, four or all eight warps have
+// a group of 8 sinks each and work on each other's rows, so that the rows are read
+// once for 64 sinks and not for 8 (backward of 8192 tokens, 16/4 heads, window 128,
+// 32 sinks: 170 -> 150 us, 128 sinks: 319 -> 255). The warps' fp32 sums are
 // joined in a fixed order and written per run; the key-major kernel adds the runs of
 // each sink in order in its epilogue, or, where they are many, their sums, which a
 // second kernel makes in a fixed order. No atomics: the result does not depend on
@@ -51,7 +54,7 @@ struct FarCfg {
   static constexpr int kRowBytes = D * 2;
   static constexpr int kChunks = D / 8;  // 16-byte chunks of a row
   static constexpr int kHalf = 16 * kRowBytes;
-  static constexpr int kStageBytes = 2 * kHalf;  // a warp's 16 rows of Q, then of dO
+  static constexpr int kStageBytes = 2 * kHalf + 128;  // a warp's 16 rows of Q, of dO, and of the two tables
   static constexpr int kWarpBytes = kStages * kStageBytes;
   static constexpr int kSmemBytes = kWarps * kWarpBytes;
   static_assert(kGroup * 2 * D * 4 <= kWarpBytes, "a warp's sums fit over its buffers");
@@ -84,14 +87,29 @@ __global__ void __launch_bounds__(kThreads, 1) far_kernel(const FarArgs a) {
     // band ends grow with the key: tiles from here on have far sinks
     const int mf = max(m0, last_qtile(g, lo / kBN) + 1);
     if (mf >= m1) continue;
-    float* part = a.part + ((static_cast<size_t>(b) * g.Hkv + gl) * g.n_tiles + m0) * g.ns * (2 * D);
+    float* out = a.part + ((static_cast<size_t>(b) * g.Hkv + gl) * g.n_tiles + m0) * g.ns * (2 * D);
     const int steps = (m1 - mf) * g.G;
 
-    for (int s0 = 0; s0 < n_sinks; s0 += kGroup) {
+    // `team` neighbouring warps work on each other's rows, each for its own 8 sinks
+    const int team = n_sinks <= kGroup ? 1 : n_sinks <= 2 * kGroup ? 2 : n_sinks <= 4 * kGroup ? 4 : 8;
+    const int part = warp / team, member = warp - part * team;
+    auto team_sync = [&]() {
+      if (team == 1)
+        __syncwarp();
+      else
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + part), "r"(32 * team) : "memory");
+    };
+
+    for (int sb = 0; sb < n_sinks; sb += kGroup * team) {
+      const int s0 = sb + member * kGroup;  // this warp's sinks
       auto fetch = [&](int st) {
         if (st < steps) {
           const int h = gl * g.G + st % g.G, row0 = (mf + st / g.G) * kBM + warp * 16;
           const uint32_t dst = mine + (st % kStages) * C::kStageBytes;
+          if (lane < 8) {
+            const float* tab = (lane < 4 ? a.lse2 : a.delta) + (static_cast<size_t>(b) * g.Hq + h) * a.Lp + row0;
+            cp_async16(dst + 2 * C::kHalf + lane * 16, tab + (lane & 3) * 4, true);
+          }
 #pragma unroll
           for (int y = 0; y < 16 * C::kChunks / 32; ++y) {
             const int r = y * (32 / C::kChunks) + lane / C::kChunks, ch = lane % C::kChunks;
@@ -132,57 +150,55 @@ __global__ void __launch_bounds__(kThreads, 1) far_kernel(const FarArgs a) {
         for (int e = 0; e < 4; ++e) av[x][e] = ak[x][e] = 0.f;
 
       for (int st = 0; st < steps; ++st) {
+        cp_async_wait<kStages - 2>();
+        team_sync();  // the step's rows are there, and every warp is done with the stage that is filled next
         fetch(st + kStages - 1);
-        const int h = gl * g.G + st % g.G, m = mf + st / g.G;
-        const int i0 = m * kBM + warp * 16 + (lane >> 2);
-        const size_t tab = (static_cast<size_t>(b) * g.Hq + h) * a.Lp + i0;
-        float nl[2], nd[2];
+        const int m = mf + st / g.G;
+        for (int w = part * team; w < part * team + team && s0 < n_sinks; ++w) {  // the rows that warp w has fetched
+          const uint32_t sq = base + w * C::kWarpBytes + (st % kStages) * C::kStageBytes, sd = sq + C::kHalf;
+          const float* tab = reinterpret_cast<const float*>(smem + (sd + C::kHalf - base)) + (lane >> 2);
+          const int i0 = m * kBM + w * 16 + (lane >> 2);
+          const float nl[2] = {tab[0], tab[8]}, nd[2] = {tab[16], tab[24]};
+          // S = Q K^T, dP = dO V^T of 16 rows and 8 sinks, even and odd steps apart
+          float sc[2][4] = {}, dp[2][4] = {};
+          const int ar = lane & 15, ac = lane >> 4;  // rows and half chunks of the fragments
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          nl[half] = a.lse2[tab + half * 8];
-          nd[half] = a.delta[tab + half * 8];
-        }
-        cp_async_wait<kStages - 1>();
-        __syncwarp();
-        const uint32_t sq = mine + (st % kStages) * C::kStageBytes, sd = sq + C::kHalf;
-        // S = Q K^T, dP = dO V^T of 16 rows and 8 sinks, even and odd steps apart
-        float sc[2][4] = {}, dp[2][4] = {};
-        const int ar = lane & 15, ac = lane >> 4;  // rows and half chunks of the fragments
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          uint32_t qa[4], da[4];
-          ldsm_x4(qa, sq + at<D>(ar, 2 * kk + ac));
-          ldsm_x4(da, sd + at<D>(ar, 2 * kk + ac));
-          mma_16816(sc[kk & 1], qa, kb[kk][0], kb[kk][1]);
-          mma_16816(dp[kk & 1], da, vb[kk][0], vb[kk][1]);
-        }
-        uint32_t pt[2], dt[2];  // P, dS as B fragments: rows x sinks, rows 0..7 and 8..15
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {   // rows i0, i0 + 8
-          const bool live = i0 + half * 8 < hi;  // a row of the same document (hi <= S)
-          float p[2], ds[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float sv = sc[0][half * 2 + e] + sc[1][half * 2 + e], dv = dp[0][half * 2 + e] + dp[1][half * 2 + e];
-            p[e] = live && m >= far_from[e] ? ex2_approx(sv * g.scale_log2 + nl[half]) : 0.f;
-            ds[e] = p[e] * (dv + nd[half]);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t qa[4], da[4];
+            ldsm_x4(qa, sq + at<D>(ar, 2 * kk + ac));
+            ldsm_x4(da, sd + at<D>(ar, 2 * kk + ac));
+            mma_16816(sc[kk & 1], qa, kb[kk][0], kb[kk][1]);
+            mma_16816(dp[kk & 1], da, vb[kk][0], vb[kk][1]);
           }
-          // bf16 operands, as P and dS have in the key-major kernel; sums stay fp32
-          pt[half] = mov_trans(pack_bf16x2(p[0], p[1]));
-          dt[half] = mov_trans(pack_bf16x2(ds[0], ds[1]));
-        }
-        // A fragments of dO^T, Q^T: the transposed 8x8 blocks, element octets by row octets
-        const int tr = (lane & 7) + ((lane >> 4) << 3), tc = (lane >> 3) & 1;
+          uint32_t pt[2], dt[2];  // P, dS as B fragments: rows x sinks, rows 0..7 and 8..15
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          uint32_t da[4], qa[4];
-          ldsm_x4_trans(da, sd + at<D>(tr, 2 * x + tc));
-          ldsm_x4_trans(qa, sq + at<D>(tr, 2 * x + tc));
-          mma_16816(av[x], da, pt[0], pt[1]);
-          mma_16816(ak[x], qa, dt[0], dt[1]);
+          for (int half = 0; half < 2; ++half) {   // rows i0, i0 + 8
+            const bool live = i0 + half * 8 < hi;  // a row of the same document (hi <= S)
+            float p[2], ds[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float sv = sc[0][half * 2 + e] + sc[1][half * 2 + e], dv = dp[0][half * 2 + e] + dp[1][half * 2 + e];
+              p[e] = live && m >= far_from[e] ? ex2_approx(sv * g.scale_log2 + nl[half]) : 0.f;
+              ds[e] = p[e] * (dv + nd[half]);
+            }
+            // bf16 operands, as P and dS have in the key-major kernel; sums stay fp32
+            pt[half] = mov_trans(pack_bf16x2(p[0], p[1]));
+            dt[half] = mov_trans(pack_bf16x2(ds[0], ds[1]));
+          }
+          // A fragments of dO^T, Q^T: the transposed 8x8 blocks, element octets by row octets
+          const int tr = (lane & 7) + ((lane >> 4) << 3), tc = (lane >> 3) & 1;
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) {
+            uint32_t da[4], qa[4];
+            ldsm_x4_trans(da, sd + at<D>(tr, 2 * x + tc));
+            ldsm_x4_trans(qa, sq + at<D>(tr, 2 * x + tc));
+            mma_16816(av[x], da, pt[0], pt[1]);
+            mma_16816(ak[x], qa, dt[0], dt[1]);
+          }
         }
-        __syncwarp();  // every lane has read the stage before it is filled again
       }
+      cp_async_wait<0>();
+      __syncthreads();  // every warp is done with the buffers
       // the warps' sums over their own buffers, then added warp by warp
       float* mysum = reinterpret_cast<float*>(smem + warp * C::kWarpBytes);
 #pragma unroll
@@ -194,12 +210,13 @@ __global__ void __launch_bounds__(kThreads, 1) far_kernel(const FarArgs a) {
           mysum[(s * 2 + 1) * D + d] = av[x][e];
         }
       __syncthreads();
-      const int n = min(kGroup, n_sinks - s0) * 2 * D;
+      const int n = min(kGroup * team, n_sinks - sb) * 2 * D;
       for (int x = tid; x < n; x += kThreads) {
+        constexpr int kOne = kGroup * 2 * D;  // a warp's sums
+        const int who = x / kOne;
         float t = 0.f;
-#pragma unroll
-        for (int y = 0; y < kWarps; ++y) t += reinterpret_cast<const float*>(smem + y * C::kWarpBytes)[x];
-        part[static_cast<size_t>(s0) * 2 * D + x] = t;
+        for (int y = who; y < kWarps; y += team) t += reinterpret_cast<const float*>(smem + y * C::kWarpBytes)[x - who * kOne];
+        out[static_cast<size_t>(sb) * 2 * D + x] = t;
       }
       __syncthreads();  // read before the buffers are filled again
     }
