@@ -18,8 +18,8 @@
 // wait for P^T and dS^T, which the same warps write after them.
 //
 // Bound by the chain S^T -> P^T -> dV -> S^T (1.8 us per step; the four products take
-// 1.1) and by about 6 us per item. B=1 S=32768 H=16/4 D=128 W=2048, 4 sinks: 890 us,
-// 1199 TFLOP/s (8 D flops per visible pair).
+// 1.1) and by about 5 us per item (64 KB of stores among them). B=1 S=32768 H=16/4 D=128
+// W=2048, 4 sinks: 870 us, 1227 TFLOP/s (8 D flops per visible pair).
 #include <math.h>
 
 #include "usp_ptx.cuh"

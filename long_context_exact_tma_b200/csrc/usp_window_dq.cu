@@ -23,9 +23,10 @@
 // item, whose first dQ product waits for dS, written by the warps that read this
 // item's dQ before it.
 //
-// Bound by the chain dP -> dS -> dQ (1.25 to 1.4 us per key tile; the three products
-// take 0.8) and by about 4 us per item. B=1 S=32768 H=16/4 D=128 W=2048, 4 sinks:
-// 795 us, 1007 TFLOP/s (6 D flops per visible pair).
+// Bound by the compute warps' own work (about 1500 cycles per key tile, as much as the
+// three products; the two overlap but for the handing over: 1.25 to 1.4 us) and by about
+// 3.5 us per item (masked tiles, epilogue, the next item's rows). B=1 S=32768 H=16/4 D=128
+// W=2048, 4 sinks: 761 us, 1052 TFLOP/s (6 D flops per visible pair).
 #include <math.h>
 
 #include "usp_ptx.cuh"

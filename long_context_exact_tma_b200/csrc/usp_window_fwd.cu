@@ -24,9 +24,9 @@
 //
 // Bound by the chain S -> softmax -> PV -> S of each query tile, two of which
 // alternate (1.86 us per key tile of a pair; the products alone take 1.1), and by
-// about 6 us per item (first scores, masked edges, epilogue). B=1 S=32768 H=16/4
-// D=128 W=2048, 4 sinks: 554 us, 963 TFLOP/s of visible pairs; S=16384 H=32/8 W=1024:
-// 335 us, 798 TFLOP/s.
+// about 4 us per item (first scores, masked edges, 64 KB of stores). B=1 S=32768 H=16/4
+// D=128 W=2048, 4 sinks: 537 us, 994 TFLOP/s of visible pairs; S=16384 H=32/8 W=1024:
+// 315 us, 849 TFLOP/s.
 #include <math.h>
 
 #include "usp_ptx.cuh"

@@ -17,12 +17,12 @@
 // a group of 8 sinks each and work on each other's rows, so that the rows are read
 // once for 64 sinks and not for 8 (backward of 8192 tokens, 16/4 heads, window 128,
 // 32 sinks: 170 -> 150 us, 128 sinks: 319 -> 255). The warps' fp32 sums are
-// joined in a fixed order and written per run; the key-major kernel adds the runs of
-// each sink in order in its epilogue, or, where they are many, their sums, which a
+// joined in a fixed order and written per run; the key-major kernel's items add the
+// runs of their sinks up in order, or, where they are many, take their sums, which a
 // second kernel makes in a fixed order. No atomics: the result does not depend on
 // scheduling.
 //
-// B=1 S=32768 H=16/4 D=128, 4 sinks: 53 us, 5.1 TB/s of Q and dO.
+// B=1 S=32768 H=16/4 D=128, 4 sinks: 44 us, 6.2 TB/s of Q and dO.
 #include <math.h>
 
 #include "usp_mma.cuh"
