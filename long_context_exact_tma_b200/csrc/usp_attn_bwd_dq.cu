@@ -71,7 +71,10 @@ struct DqArgs {
 struct DqBars {
   uint64_t q_full;
   uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
-  uint64_t s_full[2], dp_full, dp_free, ds_full, dq_done[2], drain;
+  uint64_t s_full[2], dp_full, dp_free, dq_done[2], drain;
+  // One per S buffer: dP of the next tile is issued ahead of the wait for dS, so a delayed issuing
+  // warp could find a single barrier two phases on, which it cannot tell from none.
+  uint64_t ds_full[2];
   // Key-tile descriptors published by the producer with k_full of that tile:
   // {1, or -1 = no more tiles; ring rank j of the key owner; key tile n; tile kind}.
   int step[4][4];
@@ -167,10 +170,10 @@ __global__ void __launch_bounds__(kThreadsDq, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->s_full[s], 1);
       mbar_init(&bars->dq_done[s], 1);
+      mbar_init(&bars->ds_full[s], kComputeDq / 32);
     }
     mbar_init(&bars->dp_full, 1);
     mbar_init(&bars->dp_free, kComputeDq / 32);  // one arrival per compute warp
-    mbar_init(&bars->ds_full, kComputeDq / 32);
     mbar_init(&bars->drain, 1);
     fence_mbar_init();
   }
@@ -330,7 +333,7 @@ __global__ void __launch_bounds__(kThreadsDq, 1)
           tc_fence_after();
           issue_dp(it + 1);
         }
-        if (!mbar_wait_w(&bars->ds_full, it & 1, w, kSiteQDs)) { ok = false; break; }
+        if (!mbar_wait_w(&bars->ds_full[it & 1], (it >> 1) & 1, w, kSiteQDs)) { ok = false; break; }
         tc_fence_after();
         const uint64_t kd = dKmn + (((it % C::kKStages) * C::kTileBytes) >> 4);
 #pragma unroll
@@ -461,7 +464,7 @@ __global__ void __launch_bounds__(kThreadsDq, 1)
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive_warp(&bars->ds_full);
+      mbar_arrive_warp(&bars->ds_full[it & 1]);
     }
     // ------------------------------------------------------------ epilogue: dQ rows
     if (ok && it >= 1)
