@@ -16,7 +16,9 @@
 // r_i sum_j P_ij k_j, which matters next to dQ's own rounding only where few keys
 // share a row's weight (the ratio falls with the root of their number: 1.2 of the
 // rounding at 4 keys, 0.4 at 64): query tiles with rows of fewer than 48 keys walk
-// the tiles of those rows' keys twice, the second time with dS = -r_i P_ij.
+// the tiles of those rows' keys twice. Where these are all tiles, the first walk only
+// finds r and the second makes dQ with Delta + r (8192 tokens, 16 heads, window 8: 73 -> 71 us
+// against two walks that both add); else the second adds dS = -r_i P_ij.
 //
 // TMEM: S / dS at 0 and 128, dP at 256, dQ at 384. The key tiles of all items of
 // a CTA form one stream: S runs two tiles and dP one tile ahead, into the next
@@ -103,6 +105,8 @@ constexpr int kFewKeys = 48;
 struct DqRun {
   KeyRun kr;
   int n1, n2, nt;
+  // the first pass adds to dQ (no second pass over all tiles follows)
+  __device__ __forceinline__ bool adds(int it) const { return it >= n1 || n2 != n1; }
   __device__ __forceinline__ int pass_it(int it) const { return it < n1 ? it : it - n2; }
   __device__ __forceinline__ int base(int it) const { return kr.base(pass_it(it)); }
   __device__ __forceinline__ int width(int it) const { return kr.width(pass_it(it)); }
@@ -280,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       v_d.next();
       return true;
     };
-    auto issue_dq = [&](int keys, bool first) -> bool {  // dQ += dS K
+    auto issue_dq = [&](int keys, bool first, bool adds) -> bool {  // dQ += dS K
       if (!mbar_wait_w(&bars->ds_full[q_turn & 1], (q_turn >> 1) & 1, w, kSiteDs)) return false;
       tc_fence_after();
       const uint64_t kd = dKmn + ((k_q.at * C::kTileBytes) >> 4);
@@ -289,7 +293,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_bf16_tmem_a_w(tmem + kColDQ, ds + (kk < 4 ? 0u : 64u) + (kk & 3) * 8, kd + ((kk * 16 * 128) >> 4), kIdKM,
                            (!first || kk > 0) ? 1u : 0u);
       };
-      if (keys == kBN) {
+      if (!adds) {
+        // (the warps have read the tile: its buffers are free)
+      } else if (keys == kBN) {
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk) step(kk);
       } else {
@@ -326,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = issue_dp(width(it + 1));
           if (it + 2 == nt) umma_commit_w(&bars->do_empty);
         }
-        ok = ok && issue_dq(width(it), it == 0);
+        ok = ok && issue_dq(width(it), it == (r.n2 == r.n1 ? r.n1 : 0), r.adds(it));
         if (ok && it + 2 < nt) {  // S two tiles ahead
           ok = issue_s(width(it + 2));
           if (it + 3 == nt) umma_commit_w(&bars->q_empty);
@@ -364,7 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t tab = (static_cast<size_t>(x.b) * g.Hq + x.h) * a.Lp + i;  // Lp covers the whole tile
       const float nl = a.lse2[tab];  // -inf on padding rows: their P is 0
       const float nd = a.delta[tab];
-      const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
+      const float2 nl2 = make_float2(nl, nl);
+      float2 nd2 = make_float2(nd, nd), z2 = make_float2(1.f, 1.f);  // dS = P (z dP + nd)
       // visible keys of the row: [first, end) and the sinks [lo, sink_end); none past the end
       const int lo = store ? win_lo(g, i) : 1 << 30, end = i + 1;
       const int first = max(lo, i - g.W + 1), sink_end = min(lo + g.ns, i + 1);
@@ -372,15 +379,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int q_last = min(x.q0 + kBM, g.S) - 1;
       const int first_all = max(win_lo(g, q_last), q_last - g.W + 1);
       float2 res2 = make_float2(0.f, 0.f);
-      float res = 0.f, fix = 0.f;
+      float res = 0.f;
       for (int it = 0; it < kr.nt; ++it, ++n) {
         if (it == kr.n1) {  // the second pass needs the row's residue
           ok = __all_sync(0xffffffffu, mbar_wait(&bars->r_full, item & 1, w, kSiteRes));
           if (!ok) break;
           const float* s = sRes + (item & 1) * 256 + row;
           res = s[0] + s[128];
-          // (the repeated tiles hold all keys of the rows of few, and only of those)
-          fix = g.W + g.ns < kFewKeys || i - lo + 1 < kFewKeys ? -res : 0.f;
+          if (kr.n2 == kr.n1) {
+            nd2 = make_float2(nd - res, nd - res);
+          } else {  // the repeated tiles hold all keys of the rows of few, and only of those
+            const float fix = i - lo + 1 < kFewKeys ? -res : 0.f;
+            nd2 = make_float2(fix, fix);
+            z2 = make_float2(0.f, 0.f);
+          }
         }
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[n & 1], (n >> 1) & 1, w, kSiteS));
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->dp_full, n & 1, w, kSiteDp));
@@ -413,24 +425,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (width != kBN) hide_columns(rp, vis, 0u);
           }
           uint32_t dk[16];
-          if (it < kr.n1) {
 #pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              const float2 y = ffma2(make_float2(__uint_as_float(rs[c]), __uint_as_float(rs[c + 1])), sl2, nl2);
-              const float2 pv = make_float2(ex2_approx(y.x), ex2_approx(y.y));  // -inf -> 0
-              const float2 ds =
-                  fmul2(pv, fadd2(make_float2(__uint_as_float(rp[c]), __uint_as_float(rp[c + 1])), nd2));
-              res2 = fadd2(res2, ds);
-              dk[c >> 1] = pack_bf16x2(ds.x, ds.y);
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              const float2 y = ffma2(make_float2(__uint_as_float(rs[c]), __uint_as_float(rs[c + 1])), sl2, nl2);
-              dk[c >> 1] = pack_bf16x2(fix * ex2_approx(y.x), fix * ex2_approx(y.y));
-            }
+          for (int c = 0; c < 32; c += 2) {
+            const float2 y = ffma2(make_float2(__uint_as_float(rs[c]), __uint_as_float(rs[c + 1])), sl2, nl2);
+            const float2 pv = make_float2(ex2_approx(y.x), ex2_approx(y.y));  // -inf -> 0
+            const float2 ds =
+                fmul2(pv, ffma2(make_float2(__uint_as_float(rp[c]), __uint_as_float(rp[c + 1])), z2, nd2));
+            res2 = fadd2(res2, ds);
+            dk[c >> 1] = pack_bf16x2(ds.x, ds.y);
           }
-          tmem_st16(trow + cS + cbase + (c0 - cbase) / 2, dk);
+          if (kr.adds(it)) tmem_st16(trow + cS + cbase + (c0 - cbase) / 2, dk);
         }
         if (it + 1 == kr.n1) sRes[(item & 1) * 256 + wg * 128 + row] = res2.x + res2.y;
         tmem_st_wait();
