@@ -32,7 +32,9 @@ constexpr int kThreads = 320;
 constexpr int kComputeWarps = 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColDP = 128, kColDV = 256, kColDK = 384;
-constexpr int kPolyPer8 = 2;  // key pairs (of every 8) whose exp2 runs on the FMA pipe, as in the mesh kernel
+// Key pairs (of every 8) whose exp2 runs on the FMA pipe: backward of 8192 tokens, 16/4 heads, window 2048,
+// with 0, 2, 3, 4: 434, 428, 429, 434 us (D=64: 371, 363, 362, 364).
+constexpr int kPolyPer8 = 2;
 
 template <int D>
 struct Cfg {
