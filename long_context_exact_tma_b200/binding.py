@@ -39,6 +39,7 @@ USP_MAX_ROWS_JOBS = 16
 USP_MAX_ROPE_JOBS = 4
 USP_ROPE_MAX_R = 256
 USP_WINDOW_MAX_SINKS = 128
+USP_WINDOW_FWD_WS = 256  # usp_window_workspace_size of a forward: the status header
 USP_WINDOW_MAX_NEW = 16
 
 

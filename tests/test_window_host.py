@@ -52,7 +52,7 @@ def test_pointers_and_workspaces_are_refused(call, n):
 
 def test_workspace_sizes():
     ws = B_.usp_window_workspace_size
-    assert ws(1, 100, 4, 2, 64, 10, 2, 0, 0) == 256
+    assert ws(1, 100, 4, 2, 64, 10, 2, 0, 0) == ws(3, 9000, 64, 1, 128, 99, 128, 7, 0) == B_.USP_WINDOW_FWD_WS
     tables = 2 * 4 * (1 * 4 * 128)
     assert ws(1, 100, 4, 2, 64, 10, 0, 0, 1) == 256 + tables
     assert ws(1, 100, 4, 2, 64, 100, 2, 0, 1) == 256 + tables            # nobody is far from a sink
