@@ -624,7 +624,8 @@ int usp_workspace_status(void* workspace, int* site, void* stream);
 
 /*
  * Limit of every bounded device wait launched by this thread from now on, in
- * nanoseconds (default 2e9). A test hook: a very small limit makes waits give up.
+ * nanoseconds (default 2e9). A test hook: with 0, a wait gives up that is not over
+ * when it is first looked at.
  */
 void usp_set_wait_limit_ns(unsigned long long ns);
 

@@ -66,7 +66,8 @@ struct WaitCtl {
 // the abort flag and records `site` in the status word).
 // The status word (a global load of several hundred cycles) and the timer are
 // read only every 32nd round, so that a phase completing is seen within one
-// try_wait and not after a global round trip. Only the first try_wait is
+// try_wait and not after a global round trip; with a limit of 0 the caller's one
+// try_wait is all. Only the first try_wait is
 // inlined at each wait site; the polling loop is one out-of-line function, so
 // the many wait sites of a warp-specialised kernel keep its hot loops small
 // (the warps of all roles share each SM sub-partition's instruction cache).
@@ -74,15 +75,15 @@ static __device__ __noinline__ bool mbar_wait_poll(uint32_t a, uint32_t parity, 
                                                    uint64_t limit_ns, int site) {
   uint64_t t0 = 0;
   for (uint32_t n = 1;; ++n) {
-    if (mbar_try_wait(a, parity)) return true;
+    if (limit_ns != 0 && mbar_try_wait(a, parity)) return true;
     if (*abort_flag) return false;
-    if ((n & 31u) == 0u) {
+    if ((n & 31u) == 0u || limit_ns == 0) {
       if (*reinterpret_cast<volatile int*>(status) != 0) {  // another CTA already gave up
         *abort_flag = 1;
         return false;
       }
       const uint64_t now = global_timer_ns();
-      if (t0 == 0) {
+      if (t0 == 0 && limit_ns != 0) {
         t0 = now;
       } else if (now - t0 > limit_ns) {
         *abort_flag = 1;

@@ -145,8 +145,8 @@ __device__ __forceinline__ void store_rows32(__nv_bfloat16* base, size_t row_ste
   }
 }
 
-// The limit of the waits that let a warp's own copies and products land after a CTA has given up:
-// not the caller's limit, which may be shorter than a copy takes.
+// The limit of the waits that let a warp's own copies and products land before a CTA ends (it may have
+// given up meanwhile): not the caller's limit, which may be shorter than a copy takes.
 constexpr unsigned long long kDrainNs = 2000000000ull;
 
 // ---------------------------------------------------------------- work items

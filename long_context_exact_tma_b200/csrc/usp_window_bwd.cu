@@ -206,11 +206,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (*reinterpret_cast<volatile int*>(&bars->abort_flag)) {
-      if (n_kv > 0) mbar_wait_drain(&bars->kv_full, (n_kv - 1) & 1, kDrainNs);
-      for (int it = issued - C::kStages < 0 ? 0 : issued - C::kStages; it < issued; ++it)
-        mbar_wait_drain(&bars->qd_full[it % C::kStages], (it / C::kStages) & 1, kDrainNs);
-    }
+    // Every copy this warp started lands before the CTA ends, whoever may have given up since.
+    if (n_kv > 0) mbar_wait_drain(&bars->kv_full, (n_kv - 1) & 1, kDrainNs);
+    for (int it = issued - C::kStages < 0 ? 0 : issued - C::kStages; it < issued; ++it)
+      mbar_wait_drain(&bars->qd_full[it % C::kStages], (it / C::kStages) & 1, kDrainNs);
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ UMMA issuer
@@ -292,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (!ok && issued_any) {
+    if (issued_any) {  // the products too: the warps that wait for the last ones may have given up
       umma_commit_w(&bars->drain);
       mbar_wait_drain(&bars->drain, 0, kDrainNs);
     }

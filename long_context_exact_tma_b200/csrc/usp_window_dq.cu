@@ -223,14 +223,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++nv;
       }
     }
-    if (*reinterpret_cast<volatile int*>(&bars->abort_flag)) {
-      if (n_q > 0) mbar_wait_drain(&bars->q_full, (n_q - 1) & 1, kDrainNs);
-      if (n_do > 0) mbar_wait_drain(&bars->do_full, (n_do - 1) & 1, kDrainNs);
-      for (int it = nk - C::kKSt < 0 ? 0 : nk - C::kKSt; it < nk; ++it)
-        mbar_wait_drain(&bars->k_full[it % C::kKSt], (it / C::kKSt) & 1, kDrainNs);
-      for (int it = nv - C::kVSt < 0 ? 0 : nv - C::kVSt; it < nv; ++it)
-        mbar_wait_drain(&bars->v_full[it % C::kVSt], (it / C::kVSt) & 1, kDrainNs);
-    }
+    // Every copy this warp started lands before the CTA ends, whoever may have given up since.
+    if (n_q > 0) mbar_wait_drain(&bars->q_full, (n_q - 1) & 1, kDrainNs);
+    if (n_do > 0) mbar_wait_drain(&bars->do_full, (n_do - 1) & 1, kDrainNs);
+    for (int it = nk - C::kKSt < 0 ? 0 : nk - C::kKSt; it < nk; ++it)
+      mbar_wait_drain(&bars->k_full[it % C::kKSt], (it / C::kKSt) & 1, kDrainNs);
+    for (int it = nv - C::kVSt < 0 ? 0 : nv - C::kVSt; it < nv; ++it)
+      mbar_wait_drain(&bars->v_full[it % C::kVSt], (it / C::kVSt) & 1, kDrainNs);
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ UMMA issuer
@@ -347,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = ok && mbar_wait_w(&bars->do_full, item & 1, w, kSiteDo) && issue_dp(r.width(0));
       if (ok && r.nt == 1) umma_commit_w(&bars->do_empty);
     }
-    if (!ok && issued_any) {
+    if (issued_any) {  // the products too: the warps that wait for the last ones may have given up
       umma_commit_w(&bars->drain);
       mbar_wait_drain(&bars->drain, 0, kDrainNs);
     }
