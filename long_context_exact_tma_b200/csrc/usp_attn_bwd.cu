@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
         tma_load_4d_w(&tm_v, &bars->kv_full, sV + p * C::kPanelBytes, p * 64, gl, k0, krb);
       }
       int issued = 0;
+      bool ended = false;  // the end of the walk is on the barrier of the oldest stage: that copy has landed
       const MaskedQ mq{g, b, u, gl, kmin, kmax};
       // sub-problem mode: the launch's q-heads are a.sub.h0 + k * a.sub.h_step
       QWalk qw = qwalk_begin<kMask, kSub>(g, j, kmin, kmax, mq, t_lo, t_hi, gl * g.G, a.sub.h0, a.sub.h_step);
@@ -298,6 +299,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
           if (lane == 0) slot[0] = -1;
           __syncwarp();
           mbar_arrive_w(&bars->qd_full[s]);
+          ended = true;
           break;
         }
         if (lane == 0) {
@@ -325,11 +327,10 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
         ++issued;
         qwalk_next<kMask, kSub>(g, j, kmin, kmax, qw, mq, t_lo, t_hi, gl * g.G, a.sub.h0, a.sub.h_step);
       }
-      if (*reinterpret_cast<volatile int*>(&bars->abort_flag)) {
-        mbar_wait_drain(&bars->kv_full, 0, a.wait_ns);
-        for (int it = issued - C::kStages < 0 ? 0 : issued - C::kStages; it < issued; ++it)
-          mbar_wait_drain(&bars->qd_full[it % C::kStages], (it / C::kStages) & 1, a.wait_ns);
-      }
+      // Every copy this warp started lands before the CTA ends, whoever may have given up since.
+      mbar_wait_drain(&bars->kv_full, 0);
+      for (int it = max(issued - C::kStages + (ended ? 1 : 0), 0); it < issued; ++it)
+        mbar_wait_drain(&bars->qd_full[it % C::kStages], (it / C::kStages) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -407,9 +408,9 @@ __global__ void __launch_bounds__(kThreadsBwd, 1)
         issue_xt(kColDP, dV0, dDO0, s1);
         umma_commit_w(&bars->dp_full);
       }
-      if (!ok && issued_any) {
+      if (issued_any) {  // the products too: the warps that wait for the last ones may have given up
         umma_commit_w(&bars->drain);
-        mbar_wait_drain(&bars->drain, 0, a.wait_ns);
+        mbar_wait_drain(&bars->drain, 0);
       }
     }
     __syncwarp();

@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(kThreadsDq, 1)
         tma_load_4d_w(&tm_do, &bars->q_full, sDO + p * C::kPanelBytes, p * 64, h, q0, qrb);
       }
       int k_issued = 0, v_issued = 0;
+      bool ended = false;  // the end of the walk is on the barrier of the oldest K stage: that copy has landed
       while (true) {
         const int it = k_issued;
         const int sk = it % C::kKStages, sv = it % C::kVStages;
@@ -230,6 +231,7 @@ __global__ void __launch_bounds__(kThreadsDq, 1)
           if (lane == 0) slot[0] = -1;
           __syncwarp();
           mbar_arrive_w(&bars->k_full[sk]);
+          ended = true;
           break;
         }
         if (lane == 0) {
@@ -258,14 +260,13 @@ __global__ void __launch_bounds__(kThreadsDq, 1)
         else
           kv_walk_next<kSub>(g, i, qmin, qmax, t_hi, kw);
       }
-      if (*reinterpret_cast<volatile int*>(&bars->abort_flag)) {
-        // Let every copy this warp started land before the CTA exits.
-        mbar_wait_drain(&bars->q_full, 0, a.wait_ns);
-        for (int it = k_issued - C::kKStages < 0 ? 0 : k_issued - C::kKStages; it < k_issued; ++it)
-          mbar_wait_drain(&bars->k_full[it % C::kKStages], (it / C::kKStages) & 1, a.wait_ns);
-        for (int it = v_issued - C::kVStages < 0 ? 0 : v_issued - C::kVStages; it < v_issued; ++it)
-          mbar_wait_drain(&bars->v_full[it % C::kVStages], (it / C::kVStages) & 1, a.wait_ns);
-      }
+      // Every copy this warp started lands before the CTA ends, whoever may have given up since, and where
+      // there is no key tile, so that nobody waits for Q and dO.
+      mbar_wait_drain(&bars->q_full, 0);
+      for (int it = max(k_issued - C::kKStages + (ended ? 1 : 0), 0); it < k_issued; ++it)
+        mbar_wait_drain(&bars->k_full[it % C::kKStages], (it / C::kKStages) & 1);
+      for (int it = max(v_issued - C::kVStages, 0); it < v_issued; ++it)
+        mbar_wait_drain(&bars->v_full[it % C::kVStages], (it / C::kVStages) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -356,9 +357,9 @@ __global__ void __launch_bounds__(kThreadsDq, 1)
         }
         have1 = have2;
       }
-      if (!ok && issued_any) {
+      if (issued_any) {  // the products too: the warps that wait for the last ones may have given up
         umma_commit_w(&bars->drain);
-        mbar_wait_drain(&bars->drain, 0, a.wait_ns);
+        mbar_wait_drain(&bars->drain, 0);
       }
     }
     __syncwarp();

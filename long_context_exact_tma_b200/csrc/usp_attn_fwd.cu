@@ -248,6 +248,7 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
       else
         kw = kv_walk_begin<kSub>(g, i, qmin, qmax, t_begin, t_end);
       int issued = 0;
+      bool ended = false;  // the end of the walk is on the barrier of the oldest stage: that copy has landed
       const bool any = kw.valid;
       const int n_st = kside ? C::kKSt : C::kVSt;
       uint64_t* full = kside ? bars->k_full : bars->v_full;
@@ -280,6 +281,7 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
             if (lane == 0) slot[0] = -1;
             __syncwarp();
             mbar_arrive_w(&full[s]);
+            ended = true;
             break;
           }
           const int kinds = kMask ? kw.kind
@@ -303,12 +305,10 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
         else
           kv_walk_next<kSub>(g, i, qmin, qmax, t_end, kw);
       }
-      if (*reinterpret_cast<volatile int*>(&bars->abort_flag)) {
-        // Let every copy this warp started land before the CTA exits.
-        if (any && kside) mbar_wait_drain(&bars->q_full, 0, a.wait_ns);
-        for (int it = issued - n_st < 0 ? 0 : issued - n_st; it < issued; ++it)
-          mbar_wait_drain(&full[it % n_st], (it / n_st) & 1, a.wait_ns);
-      }
+      // Every copy this warp started lands before the CTA ends, whoever may have given up since.
+      if (any && kside) mbar_wait_drain(&bars->q_full, 0);
+      for (int it = max(issued - n_st + (ended ? 1 : 0), 0); it < issued; ++it)
+        mbar_wait_drain(&full[it % n_st], (it / n_st) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -486,9 +486,9 @@ __global__ void __launch_bounds__(kThreadsFwd, 1)
           if (!ok || !next) break;
         }
       }
-      if (!ok && issued_any) {
+      if (issued_any) {  // the products too: the warps that wait for the last ones may have given up
         umma_commit_w(&bars->drain);
-        mbar_wait_drain(&bars->drain, 0, a.wait_ns);
+        mbar_wait_drain(&bars->drain, 0);
       }
     }
     __syncwarp();

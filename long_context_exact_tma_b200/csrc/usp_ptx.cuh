@@ -99,12 +99,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
   return mbar_wait_poll(a, parity, w.abort_flag, w.status, w.limit_ns, site);
 }
 
-// Drain wait used after an abort: ignores the abort flag, gives up after limit_ns.
-__device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+// Lets a warp's own copies and products land before the CTA ends (it may have given up meanwhile): ignores
+// the abort flag, and has a limit of its own, since the caller's may be shorter than a copy takes.
+constexpr uint64_t kDrainNs = 2000000000ull;
+__device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_addr(bar);
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait(a, parity)) {
-    if (global_timer_ns() - t0 > limit_ns) return false;
+    if (global_timer_ns() - t0 > kDrainNs) return false;
   }
   return true;
 }

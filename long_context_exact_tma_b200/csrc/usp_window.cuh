@@ -145,10 +145,6 @@ __device__ __forceinline__ void store_rows32(__nv_bfloat16* base, size_t row_ste
   }
 }
 
-// The limit of the waits that let a warp's own copies and products land before a CTA ends (it may have
-// given up meanwhile): not the caller's limit, which may be shorter than a copy takes.
-constexpr unsigned long long kDrainNs = 2000000000ull;
-
 // ---------------------------------------------------------------- work items
 // Hands a persistent CTA its work items: the first is its block number, each next one
 // the grid's counter says when the CTA is ready for it (items differ: documents, rows

@@ -207,9 +207,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // Every copy this warp started lands before the CTA ends, whoever may have given up since.
-    if (n_kv > 0) mbar_wait_drain(&bars->kv_full, (n_kv - 1) & 1, kDrainNs);
+    if (n_kv > 0) mbar_wait_drain(&bars->kv_full, (n_kv - 1) & 1);
     for (int it = issued - C::kStages < 0 ? 0 : issued - C::kStages; it < issued; ++it)
-      mbar_wait_drain(&bars->qd_full[it % C::kStages], (it / C::kStages) & 1, kDrainNs);
+      mbar_wait_drain(&bars->qd_full[it % C::kStages], (it / C::kStages) & 1);
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ UMMA issuer
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (issued_any) {  // the products too: the warps that wait for the last ones may have given up
       umma_commit_w(&bars->drain);
-      mbar_wait_drain(&bars->drain, 0, kDrainNs);
+      mbar_wait_drain(&bars->drain, 0);
     }
     __syncwarp();
   } else {

@@ -224,12 +224,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // Every copy this warp started lands before the CTA ends, whoever may have given up since.
-    if (n_q > 0) mbar_wait_drain(&bars->q_full, (n_q - 1) & 1, kDrainNs);
-    if (n_do > 0) mbar_wait_drain(&bars->do_full, (n_do - 1) & 1, kDrainNs);
+    if (n_q > 0) mbar_wait_drain(&bars->q_full, (n_q - 1) & 1);
+    if (n_do > 0) mbar_wait_drain(&bars->do_full, (n_do - 1) & 1);
     for (int it = nk - C::kKSt < 0 ? 0 : nk - C::kKSt; it < nk; ++it)
-      mbar_wait_drain(&bars->k_full[it % C::kKSt], (it / C::kKSt) & 1, kDrainNs);
+      mbar_wait_drain(&bars->k_full[it % C::kKSt], (it / C::kKSt) & 1);
     for (int it = nv - C::kVSt < 0 ? 0 : nv - C::kVSt; it < nv; ++it)
-      mbar_wait_drain(&bars->v_full[it % C::kVSt], (it / C::kVSt) & 1, kDrainNs);
+      mbar_wait_drain(&bars->v_full[it % C::kVSt], (it / C::kVSt) & 1);
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ UMMA issuer
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (issued_any) {  // the products too: the warps that wait for the last ones may have given up
       umma_commit_w(&bars->drain);
-      mbar_wait_drain(&bars->drain, 0, kDrainNs);
+      mbar_wait_drain(&bars->drain, 0);
     }
     __syncwarp();
   } else {

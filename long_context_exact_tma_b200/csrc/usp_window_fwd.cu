@@ -251,9 +251,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && !kside) ok = feed_take(bars->feed, k, w, kSiteFeed, next);
     }
     // Every copy this warp started lands before the CTA ends, whoever may have given up since.
-    if (n_q > 0) mbar_wait_drain(&bars->q_full, (n_q - 1) & 1, kDrainNs);
+    if (n_q > 0) mbar_wait_drain(&bars->q_full, (n_q - 1) & 1);
     for (int it = issued - n_st < 0 ? 0 : issued - n_st; it < issued; ++it)
-      mbar_wait_drain(&full[it % n_st], (it / n_st) & 1, kDrainNs);
+      mbar_wait_drain(&full[it % n_st], (it / n_st) & 1);
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ UMMA issuer
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (issued_any) {  // the products too: the warps that wait for the last ones may have given up
       umma_commit_w(&bars->drain);
-      mbar_wait_drain(&bars->drain, 0, kDrainNs);
+      mbar_wait_drain(&bars->drain, 0);
     }
     __syncwarp();
   } else {

@@ -62,3 +62,40 @@ def test_window_attention_gives_up_and_goes_on(S, Hq, W, D, cuda):
         assert all(torch.equal(x, y) for x, y in zip(got, grads))
     if S == 4100:  # (the forward's waits at D = 64 may all end while they are first looked at)
         assert gave_up[1] > 0 and (gave_up[0] > 0 or D == 64), gave_up
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("S,Hq,P_u,P_r,docs", [
+    (256, 2, 1, 2, None),
+    (2048, 8, 2, 2, None),
+    (2048, 8, 2, 2, [0, 300, 301, 1500, 2048]),   # query tiles without a key tile among the masked walks
+])
+def test_mesh_attention_gives_up_and_goes_on(S, Hq, P_u, P_r, docs, D, cuda):
+    B, Hkv = 1, Hq // 2
+    q, do = (normal(s, P_r, P_u, B, S // P_r, Hq // P_u, D) for s in (1, 4))
+    k, v = (normal(s, P_r, P_u, B, S // P_r, Hkv // P_u, D) for s in (2, 3))
+    ws = api.workspace(max(B_.usp_attn_workspace_size(B, S, Hq, Hkv, D, True, P_u, P_r, 0, x) for x in (0, 1)), cuda)
+    if docs is None:
+        def fwd(**kw):
+            return api.attn_fwd(q, k, v, True, P_u, P_r, ws=ws, **kw)
+
+        def bwd(**kw):
+            return api.attn_bwd(q, k, v, out, lse, do, True, P_u, P_r, ws=ws, **kw)
+    else:
+        cu = torch.tensor(docs, dtype=torch.int32, device="cuda")
+
+        def fwd(**kw):
+            return api.attn_fwd_masked(q, k, v, True, P_u, P_r, cu_seqlens=cu, ws=ws, **kw)
+
+        def bwd(**kw):
+            return api.attn_bwd_masked(q, k, v, out, lse, do, True, P_u, P_r, cu_seqlens=cu, ws=ws, **kw)
+    out, lse = fwd(check_status=True)
+    grads = bwd(check_status=True)
+    gave_up = 0
+    for _ in range(20):
+        gave_up += give_up(fwd, ws, (0x1,))
+        o, l = fwd(check_status=True)
+        assert torch.equal(o, out) and torch.equal(l, lse)
+        gave_up += give_up(bwd, ws, (0x2, 0x3))
+        assert all(torch.equal(x, y) for x, y in zip(bwd(check_status=True), grads))
+    assert gave_up > 0 or S == 256
