@@ -7,28 +7,27 @@
 // A persistent CTA (one per SM, 320 threads) takes work items: one 128-row query
 // tile of one head.
 //   warp 0      TMA producer: Q, dO per item, K (3 stages) and V (2 stages) per key tile
-//   warp 1      UMMA issuer: S = Q K^T (two buffers), dP = dO V^T, dQ += dS K
+//   warp 1      UMMA issuer: S = Q K^T, dP = dO V^T, A += P K, B += dS K
 //   warps 2..9  two warpgroups of 64 key columns; thread = query row
 // The gradient sums of a row cancel: sum_j dS_ij = 0 with the exact Delta_i =
-// sum_j P_ij dP_ij, while dO.O of the bf16 output is off by up to 2^-8 |dO||O|. The
-// kernel adds up the residue r_i = sum_j dS_ij in fp32 and writes Delta_i + r_i back
-// to the table, for the key-major kernels that run after it. Its own sum is off by
-// r_i sum_j P_ij k_j, which matters next to dQ's own rounding only where few keys
-// share a row's weight (the ratio falls with the root of their number: 1.2 of the
-// rounding at 4 keys, 0.4 at 64): query tiles with rows of fewer than 48 keys walk
-// the tiles of those rows' keys twice. Where these are all tiles, the first walk only
-// finds r and the second makes dQ with Delta + r (8192 tokens, 16 heads, window 8: 73 -> 71 us
-// against two walks that both add); else the second adds dS = -r_i P_ij.
+// sum_j P_ij dP_ij, while dO.O of the bf16 output is off by up to 2^-8 |dO||O|. With
+// that Delta', the residue r_i = sum_j dS'_ij = Delta_i - Delta'_i (added up in fp32) and
+//   dQ_i / scale = sum_j dS'_ij k_j - r_i sum_j P_ij k_j = B_i - r_i A_i.
+// A is a fourth product beside the three, for every row: without it dQ is off by
+// r_i A_i, which stands beside a dQ that cancels alike wherever a row's keys or
+// values have much in common (one key with most of the weight, a common part,
+// repeated tokens; 10 to 50 times the rounding of dS in such rows), not only where a
+// row has few keys. r and A are good to 2^-8, so what is left of r is as small beside
+// it as a rounding. Delta_i goes back to the table, for the key-major kernels that run after.
 //
-// TMEM: S / dS at 0 and 128, dP at 256, dQ at 384. The key tiles of all items of
-// a CTA form one stream: S runs two tiles and dP one tile ahead, into the next
-// item, whose first dQ product waits for dS, written by the warps that read this
-// item's dQ before it.
+// TMEM: S / P at 0 (D=64: a second buffer at 384), dP / dS at 128, B at 256, A behind
+// it. The key tiles of all items of a CTA form one stream: the next item's first S and
+// dP are issued behind this one's last products, and its first A and B wait for P and
+// dS, written by the warps that read this item's A and B before them.
 //
-// Bound by the compute warps' own work (about 1500 cycles per key tile, as much as the
-// three products; the two overlap but for the handing over: 1.25 to 1.4 us) and by about
-// 3.5 us per item (masked tiles, epilogue, the next item's rows). B=1 S=32768 H=16/4 D=128
-// W=2048, 4 sinks: 761 us, 1052 TFLOP/s (6 D flops per visible pair).
+// Bound at D=128 by the chain S -> P -> A -> S of the one S buffer, beside four products that take
+// 1.1 us. Backward of 32768 tokens, 16/4 heads, W=2048, 4 sinks: 1916 us against 1769 with the three
+// products; W=8, where every row had walked its keys twice: 107 against 136.
 #include <math.h>
 
 #include "usp_ptx.cuh"
@@ -40,8 +39,8 @@ namespace {
 constexpr int kThreads = 320;
 constexpr int kComputeWarps = 8;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColDP = 256, kColDQ = 384;
-__host__ __device__ constexpr uint32_t col_s(int b) { return 128u * b; }
+constexpr uint32_t kColDP = 128, kColB = 256;
+__host__ __device__ constexpr uint32_t col_s(int b) { return 384u * b; }
 
 template <int D>
 struct Cfg {
@@ -50,6 +49,8 @@ struct Cfg {
   static constexpr int kTileBytes = kPanels * kPanelBytes;
   static constexpr int kKSt = 3;
   static constexpr int kVSt = 2;
+  static constexpr int kSSt = D == 64 ? 2 : 1;  // S buffers
+  static constexpr uint32_t kColA = kColB + D;
   static constexpr int kOffQ = 0;
   static constexpr int kOffDO = kTileBytes;
   static constexpr int kOffK = 2 * kTileBytes;
@@ -74,11 +75,9 @@ struct Args {
 struct Bars {
   uint64_t q_full, q_empty, do_full, do_empty;
   uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
-  uint64_t s_full[2], dp_full, dp_free, dq_done[2], drain;
-  // One per S buffer: dP of the next tile is issued ahead of the wait for dS, so the warps can
-  // finish two tiles before the issuer looks for the first one's arrivals, whose phase a single
-  // barrier would have left again by then. They cannot finish a third: its dP is issued behind.
-  uint64_t ds_full[2];
+  // One p_full per S buffer: with two, the warps can have made P of two tiles before the issuer looks for
+  // the first one's arrivals (dP of the second is on its way by then), but not of a third, whose S waits for A.
+  uint64_t s_full[2], p_full[2], p_used[2], dp_full, ds_full, ds_used, drain;
   uint64_t r_full;  // both warpgroups' residues of the item are in sRes
   ItemFeed feed;
   uint32_t tmem_base;
@@ -87,7 +86,7 @@ struct Bars {
 
 enum : int {
   kSiteQEmpty = 0x601, kSiteDoEmpty = 0x602, kSiteKEmpty = 0x603, kSiteVEmpty = 0x604, kSiteQ = 0x611, kSiteDo = 0x612,
-  kSiteK = 0x613, kSiteV = 0x614, kSiteDpFree = 0x615, kSiteDs = 0x616, kSiteDqDone = 0x617, kSiteS = 0x621,
+  kSiteK = 0x613, kSiteV = 0x614, kSitePUsed = 0x615, kSiteDs = 0x616, kSiteDsUsed = 0x617, kSiteP = 0x618, kSiteS = 0x621,
   kSiteDp = 0x622, kSiteEpi = 0x623, kSiteRes = 0x624, kSiteFeed = 0x631, kSiteAlign = 0x6FF
 };
 
@@ -99,29 +98,8 @@ __device__ __forceinline__ Item item_of(const Args& a, int idx) {
   const ItemParts p = item_parts(a.div, idx);
   return Item{p.b, p.head, (a.g.n_tiles - 1 - p.rest) * kBM};
 }
-// The item's key tiles, n1 of them, and for its rows of few keys the last n2 again
-// (such a row's keys end at the diagonal; nt in all).
-constexpr int kFewKeys = 48;
-struct DqRun {
-  KeyRun kr;
-  int n1, n2, nt;
-  // the first pass adds to dQ (no second pass over all tiles follows)
-  __device__ __forceinline__ bool adds(int it) const { return it >= n1 || n2 != n1; }
-  __device__ __forceinline__ int pass_it(int it) const { return it < n1 ? it : it - n2; }
-  __device__ __forceinline__ int base(int it) const { return kr.base(pass_it(it)); }
-  __device__ __forceinline__ int width(int it) const { return kr.width(pass_it(it)); }
-};
-__device__ __forceinline__ DqRun run_of(const WinGeo& g, const Item& x) {
-  DqRun r;
-  const int qe = min(x.q0 + kBM, g.S);
-  r.kr = key_run(g, x.q0, qe);
-  r.n1 = r.kr.nt;
-  if (g.W + g.ns < kFewKeys || x.q0 - r.kr.lo + 1 < kFewKeys)
-    r.n2 = r.n1;  // every row, or a document that starts in or just before the tile: two or three tiles
-  else
-    r.n2 = win_lo(g, qe - 1) > x.q0 ? 1 : 0;  // documents that start inside: the diagonal tile
-  r.nt = r.n1 + r.n2;
-  return r;
+__device__ __forceinline__ KeyRun run_of(const WinGeo& g, const Item& x) {
+  return key_run(g, x.q0, min(x.q0 + kBM, g.S));
 }
 
 template <int D>
@@ -155,15 +133,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->k_full[s], 1);
       mbar_init(&bars->k_empty[s], 1);
     }
-    for (int s = 0; s < C::kVSt; ++s) {
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->v_full[s], 1);
       mbar_init(&bars->v_empty[s], 1);
       mbar_init(&bars->s_full[s], 1);
-      mbar_init(&bars->dq_done[s], 1);
-      mbar_init(&bars->ds_full[s], kComputeWarps);
+      mbar_init(&bars->p_full[s], kComputeWarps);
+      mbar_init(&bars->p_used[s], 1);
     }
     mbar_init(&bars->dp_full, 1);
-    mbar_init(&bars->dp_free, kComputeWarps);
+    mbar_init(&bars->ds_full, kComputeWarps);
+    mbar_init(&bars->ds_used, 1);
     mbar_init(&bars->r_full, kComputeWarps);
     mbar_init(&bars->drain, 1);
     fence_mbar_init();
@@ -202,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int idx = blockIdx.x, next = 0;
     for (int k = 1; ok && idx < a.n_items; ++k, idx = next) {
       const Item x = item_of(a, idx);
-      const DqRun kr = run_of(g, x);
+      const KeyRun kr = run_of(g, x);
       const int kvh = x.h / g.G;
       for (int it = 0; it < kr.nt; ++it) {
         const int sk = nk % C::kKSt, sv = nv % C::kVSt;
@@ -240,10 +219,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool issued_any = false;
     // The loop below is one warp's chain of dependent steps between the products, so it
     // keeps its state in a few counters: ring positions of the K stage that S takes next
-    // and that dQ takes next, of the V stage that dP takes next, and the S buffers' turns.
+    // and that A and B take next, of the V stage that dP takes next, and tiles issued so far.
     Ring<C::kKSt> k_s, k_q;
     Ring<C::kVSt> v_d;
-    uint32_t s_turn = 0, q_turn = 0;  // tiles whose S, dQ have been issued
+    Ring<C::kSSt> s_b, p_b;             // the S buffers of S, and of A and B
+    uint32_t n_s = 0, n_d = 0, n_q = 0;  // tiles whose S; dP; A and B have been issued
     uint32_t item = 0;
     // X = A B^T of 128 rows and the first `keys` rows of B (128; 16 or 32 in a narrow tile)
     auto xt = [&](uint32_t acc, uint64_t a0, uint64_t b0, int keys) {
@@ -259,92 +239,96 @@ __global__ void __launch_bounds__(kThreads, 1)
       else
         go(idesc_bf16_f32(128, keys, 0, 0));
     };
-    auto issue_s = [&](int keys) -> bool {  // S into the buffer whose turn it is
-      if (!mbar_wait_w(&bars->k_full[k_s.at], k_s.phase, w, kSiteK)) return false;
-      // dQ two tiles back has read its dS from the buffer
-      if (s_turn >= 2 && !mbar_wait_w(&bars->dq_done[s_turn & 1], ((s_turn - 2) >> 1) & 1, w, kSiteDqDone)) return false;
-      tc_fence_after();
-      xt(tmem + col_s(s_turn & 1), dQ0, dK0 + ((k_s.at * C::kTileBytes) >> 4), keys);
-      umma_commit_w(&bars->s_full[s_turn & 1]);
-      ++s_turn;
-      k_s.next();
-      issued_any = true;
-      return true;
-    };
-    uint32_t d_turn = 0;  // tiles whose dP has been issued
-    auto issue_dp = [&](int keys) -> bool {  // dP = dO V^T, once the previous dP has been read
-      if (!mbar_wait_w(&bars->v_full[v_d.at], v_d.phase, w, kSiteV)) return false;
-      if (d_turn >= 1 && !mbar_wait_w(&bars->dp_free, (d_turn - 1) & 1, w, kSiteDpFree)) return false;
-      tc_fence_after();
-      xt(tmem + kColDP, dDO0, dV0 + ((v_d.at * C::kTileBytes) >> 4), keys);
-      umma_commit_w(&bars->dp_full);
-      umma_commit_w(&bars->v_empty[v_d.at]);
-      ++d_turn;
-      v_d.next();
-      return true;
-    };
-    auto issue_dq = [&](int keys, bool first, bool adds) -> bool {  // dQ += dS K
-      if (!mbar_wait_w(&bars->ds_full[q_turn & 1], (q_turn >> 1) & 1, w, kSiteDs)) return false;
-      tc_fence_after();
+    // acc += X K of the tile whose P or dS are in the columns from x on, packed: warpgroup c's 64 keys at 64c
+    auto xk = [&](uint32_t acc, uint32_t x, int keys, bool first) {
       const uint64_t kd = dKmn + ((k_q.at * C::kTileBytes) >> 4);
-      const uint32_t ds = tmem + col_s(q_turn & 1);
       auto step = [&](int kk) {
-        umma_bf16_tmem_a_w(tmem + kColDQ, ds + (kk < 4 ? 0u : 64u) + (kk & 3) * 8, kd + ((kk * 16 * 128) >> 4), kIdKM,
+        umma_bf16_tmem_a_w(tmem + acc, tmem + x + (kk < 4 ? 0u : 64u) + (kk & 3) * 8, kd + ((kk * 16 * 128) >> 4), kIdKM,
                            (!first || kk > 0) ? 1u : 0u);
       };
-      if (!adds) {
-        // (the warps have read the tile: its buffers are free)
-      } else if (keys == kBN) {
+      if (keys == kBN) {
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk) step(kk);
       } else {
 #pragma unroll 1
         for (int kk = 0; kk < keys / 16; ++kk) step(kk);
       }
-      umma_commit_w(&bars->dq_done[q_turn & 1]);
+    };
+    auto issue_s = [&](int keys) -> bool {  // once A has read P from the buffer
+      if (!mbar_wait_w(&bars->k_full[k_s.at], k_s.phase, w, kSiteK)) return false;
+      if (n_s >= C::kSSt && !mbar_wait_w(&bars->p_used[s_b.at], s_b.phase ^ 1u, w, kSitePUsed)) return false;
+      tc_fence_after();
+      xt(tmem + col_s(s_b.at), dQ0, dK0 + ((k_s.at * C::kTileBytes) >> 4), keys);
+      umma_commit_w(&bars->s_full[s_b.at]);
+      ++n_s;
+      s_b.next();
+      k_s.next();
+      issued_any = true;
+      return true;
+    };
+    auto issue_dp = [&](int keys) -> bool {  // dP = dO V^T, once B has read dS from its columns
+      if (!mbar_wait_w(&bars->v_full[v_d.at], v_d.phase, w, kSiteV)) return false;
+      if (n_d >= 1 && !mbar_wait_w(&bars->ds_used, (n_d - 1) & 1, w, kSiteDsUsed)) return false;
+      tc_fence_after();
+      xt(tmem + kColDP, dDO0, dV0 + ((v_d.at * C::kTileBytes) >> 4), keys);
+      umma_commit_w(&bars->dp_full);
+      umma_commit_w(&bars->v_empty[v_d.at]);
+      ++n_d;
+      v_d.next();
+      return true;
+    };
+    auto issue_a = [&](int keys, bool first) -> bool {  // A += P K
+      if (!mbar_wait_w(&bars->p_full[p_b.at], p_b.phase, w, kSiteP)) return false;
+      tc_fence_after();
+      xk(C::kColA, col_s(p_b.at), keys, first);
+      umma_commit_w(&bars->p_used[p_b.at]);
+      p_b.next();
+      return true;
+    };
+    auto issue_b = [&](int keys, bool first) -> bool {  // B += dS K
+      if (!mbar_wait_w(&bars->ds_full, n_q & 1, w, kSiteDs)) return false;
+      tc_fence_after();
+      xk(kColB, kColDP, keys, first);
+      umma_commit_w(&bars->ds_used);
       umma_commit_w(&bars->k_empty[k_q.at]);
-      ++q_turn;
+      ++n_q;
       k_q.next();
       return true;
     };
     bool ok = true;
     int idx = blockIdx.x;
-    DqRun r{};
-    if (idx < a.n_items) {
+    KeyRun r{};
+    // the first S and dP of the CTA's item number `item`, behind the last B of the one before: its Q and
+    // dO may still be on their way
+    auto begin = [&]() -> bool {
       r = run_of(g, item_of(a, idx));
-      ok = mbar_wait_w(&bars->q_full, 0, w, kSiteQ) && issue_s(r.width(0));
-      if (ok && r.nt == 1) umma_commit_w(&bars->q_empty);
-      ok = ok && mbar_wait_w(&bars->do_full, 0, w, kSiteDo) && issue_dp(r.width(0));
-      if (ok && r.nt == 1) umma_commit_w(&bars->do_empty);
-    }
+      if (!mbar_wait_w(&bars->q_full, item & 1, w, kSiteQ) || !issue_s(r.width(0))) return false;
+      if (r.nt == 1) umma_commit_w(&bars->q_empty);
+      if (!mbar_wait_w(&bars->do_full, item & 1, w, kSiteDo) || !issue_dp(r.width(0))) return false;
+      if (r.nt == 1) umma_commit_w(&bars->do_empty);
+      return true;
+    };
     while (ok && idx < a.n_items) {
-      // here the item's first S and dP have been issued
+      if (!(ok = begin())) break;
       const int nt = r.nt;
-      auto width = [&](int it) { return r.width(it); };
-      if (nt > 1) {
-        ok = issue_s(width(1));
+      if (C::kSSt == 2 && nt > 1) {
+        ok = issue_s(r.width(1));
         if (nt == 2) umma_commit_w(&bars->q_empty);
       }
       for (int it = 0; ok && it < nt; ++it) {
-        // dP of the next tile as soon as this one's has been read, ahead of dQ
-        if (it + 1 < nt) {
-          ok = issue_dp(width(it + 1));
-          if (it + 2 == nt) umma_commit_w(&bars->do_empty);
+        ok = issue_a(r.width(it), it == 0);
+        if (ok && it + C::kSSt < nt) {  // S as many tiles ahead as there are buffers
+          ok = issue_s(r.width(it + C::kSSt));
+          if (it + C::kSSt + 1 == nt) umma_commit_w(&bars->q_empty);
         }
-        ok = ok && issue_dq(width(it), it == (r.n2 == r.n1 ? r.n1 : 0), r.adds(it));
-        if (ok && it + 2 < nt) {  // S two tiles ahead
-          ok = issue_s(width(it + 2));
-          if (it + 3 == nt) umma_commit_w(&bars->q_empty);
+        ok = ok && issue_b(r.width(it), it == 0);
+        if (ok && it + 1 < nt) {
+          ok = issue_dp(r.width(it + 1));
+          if (it + 2 == nt) umma_commit_w(&bars->do_empty);
         }
       }
       ++item;
-      if (!ok || !(ok = feed_take(bars->feed, item, w, kSiteFeed, idx)) || idx >= a.n_items) break;
-      // the next item's first tile, behind this one's last dQ: its Q and dO may still be on their way
-      r = run_of(g, item_of(a, idx));
-      ok = mbar_wait_w(&bars->q_full, item & 1, w, kSiteQ) && issue_s(r.width(0));
-      if (ok && r.nt == 1) umma_commit_w(&bars->q_empty);
-      ok = ok && mbar_wait_w(&bars->do_full, item & 1, w, kSiteDo) && issue_dp(r.width(0));
-      if (ok && r.nt == 1) umma_commit_w(&bars->do_empty);
+      if (ok) ok = feed_take(bars->feed, item, w, kSiteFeed, idx);
     }
     if (issued_any) {  // the products too: the warps that wait for the last ones may have given up
       umma_commit_w(&bars->drain);
@@ -361,106 +345,117 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float2 sl2 = make_float2(g.scale_log2, g.scale_log2);
     bool ok = true;
     int n = 0, item = 0, idx = blockIdx.x;
+    Ring<C::kSSt> s_b;  // the S buffer of the tile
     for (; ok && idx < a.n_items; ++item) {
       const Item x = item_of(a, idx);
-      const DqRun kr = run_of(g, x);
+      const KeyRun kr = run_of(g, x);
       const int i = x.q0 + row;
       const bool store = i < g.S;
       const size_t tab = (static_cast<size_t>(x.b) * g.Hq + x.h) * a.Lp + i;  // Lp covers the whole tile
       const float nl = a.lse2[tab];  // -inf on padding rows: their P is 0
       const float nd = a.delta[tab];
-      const float2 nl2 = make_float2(nl, nl);
-      float2 nd2 = make_float2(nd, nd), z2 = make_float2(1.f, 1.f);  // dS = P (z dP + nd)
+      const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
       // visible keys of the row: [first, end) and the sinks [lo, sink_end); none past the end
       const int lo = store ? win_lo(g, i) : 1 << 30, end = i + 1;
       const int first = max(lo, i - g.W + 1), sink_end = min(lo + g.ns, i + 1);
-      const int w0 = kr.kr.w0 * kBN;
+      const int w0 = kr.w0 * kBN;
       const int q_last = min(x.q0 + kBM, g.S) - 1;
       const int first_all = max(win_lo(g, q_last), q_last - g.W + 1);
       float2 res2 = make_float2(0.f, 0.f);
-      float res = 0.f;
       for (int it = 0; it < kr.nt; ++it, ++n) {
-        if (it == kr.n1) {  // the second pass needs the row's residue
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->r_full, item & 1, w, kSiteRes));
-          if (!ok) break;
-          const float* s = sRes + (item & 1) * 256 + row;
-          res = s[0] + s[128];
-          if (kr.n2 == kr.n1) {
-            nd2 = make_float2(nd - res, nd - res);
-          } else {  // the repeated tiles hold all keys of the rows of few, and only of those
-            const float fix = i - lo + 1 < kFewKeys ? -res : 0.f;
-            nd2 = make_float2(fix, fix);
-            z2 = make_float2(0.f, 0.f);
-          }
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[n & 1], (n >> 1) & 1, w, kSiteS));
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->dp_full, n & 1, w, kSiteDp));
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[s_b.at], s_b.phase, w, kSiteS));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t cS = col_s(n & 1);
-        const int k0 = kr.base(it), width = kr.width(it);
+        const uint32_t cS = col_s(s_b.at);
+        const int k0 = kr.base(it), width = kr.width(it);  // a narrow tile has the first 32 columns at most
         const bool whole = k0 >= first_all && k0 + kBN - 1 <= x.q0;
-        // (one copy of the code for both halves: the kernel's instructions stay in the cache)
-        const int c_end = min(cbase + 64, width);  // a narrow tile has the first 32 columns at most: warpgroup 0
-        if (cbase >= c_end) mbar_arrive_warp(&bars->dp_free);
-#pragma unroll 1
-        for (int c0 = cbase; c0 < c_end; c0 += 32) {
-          uint32_t rs[32], rp[32];
-          tmem_ld32(trow + kColDP + c0, rp);
+        auto seen = [&](int c0) {  // (a sink tile ends where the window tiles begin)
+          return k0 < w0 ? bits_between(lo - k0, min(sink_end, w0) - k0, c0)
+                         : bits_between(first - k0, end - k0, c0) | bits_between(lo - k0, sink_end - k0, c0);
+        };
+        // Phase 1: P = exp2(s * scale * log2e - LSE * log2e) as bf16 over the S columns; the fp32 values
+        // stay in registers for dS.
+        float2 pr[32];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int c0 = cbase + half * 32;
+          if (c0 >= width) break;
+          uint32_t rs[32];
           tmem_ld32(trow + cS + c0, rs);
           tmem_ld_wait();
-          reg_fence32(rp);
           reg_fence32(rs);
-          if (c0 + 32 >= c_end) {  // the tile's dP has been read: the next one's may start
-            tc_fence_before();
-            mbar_arrive_warp(&bars->dp_free);
-          }
-          if (!whole) {
-            // (a sink tile ends where the window tiles begin)
-            const uint32_t vis = k0 < w0 ? bits_between(lo - k0, min(sink_end, w0) - k0, c0)
-                                         : bits_between(first - k0, end - k0, c0) | bits_between(lo - k0, sink_end - k0, c0);
-            hide_columns(rs, vis, kMinusInf);
-            // columns past a narrow tile's width hold what was there before (a hidden key's dP is finite: P = 0 hides it)
-            if (width != kBN) hide_columns(rp, vis, 0u);
-          }
-          uint32_t dk[16];
+          if (!whole) hide_columns(rs, seen(c0), kMinusInf);
+          uint32_t pk[16];
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
             const float2 y = ffma2(make_float2(__uint_as_float(rs[c]), __uint_as_float(rs[c + 1])), sl2, nl2);
             const float2 pv = make_float2(ex2_approx(y.x), ex2_approx(y.y));  // -inf -> 0
-            const float2 ds =
-                fmul2(pv, ffma2(make_float2(__uint_as_float(rp[c]), __uint_as_float(rp[c + 1])), z2, nd2));
+            pr[half * 16 + (c >> 1)] = pv;
+            pk[c >> 1] = pack_bf16x2(pv.x, pv.y);
+          }
+          tmem_st16(trow + cS + cbase + half * 16, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(&bars->p_full[s_b.at]);
+        s_b.next();
+        // Phase 2: dS' = P (dP - Delta') as bf16 over the dP columns, and its sum
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->dp_full, n & 1, w, kSiteDp));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int c0 = cbase + half * 32;
+          if (c0 >= width) break;
+          uint32_t rp[32];
+          tmem_ld32(trow + kColDP + c0, rp);
+          tmem_ld_wait();
+          reg_fence32(rp);
+          // columns past a narrow tile's width hold what was there before (a hidden key's dP is finite: P = 0 hides it)
+          if (width != kBN) hide_columns(rp, seen(c0), 0u);
+          uint32_t dk[16];
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float2 ds = fmul2(pr[half * 16 + (c >> 1)],
+                                    fadd2(make_float2(__uint_as_float(rp[c]), __uint_as_float(rp[c + 1])), nd2));
             res2 = fadd2(res2, ds);
             dk[c >> 1] = pack_bf16x2(ds.x, ds.y);
           }
-          if (kr.adds(it)) tmem_st16(trow + cS + cbase + (c0 - cbase) / 2, dk);
+          tmem_st16(trow + kColDP + cbase + half * 16, dk);
         }
-        if (it + 1 == kr.n1) sRes[(item & 1) * 256 + wg * 128 + row] = res2.x + res2.y;
+        if (it + 1 == kr.nt) sRes[(item & 1) * 256 + wg * 128 + row] = res2.x + res2.y;
         tmem_st_wait();
         tc_fence_before();
-        if (it + 1 == kr.n1) mbar_arrive_warp(&bars->r_full);
-        mbar_arrive_warp(&bars->ds_full[n & 1]);
+        if (it + 1 == kr.nt) mbar_arrive_warp(&bars->r_full);
+        mbar_arrive_warp(&bars->ds_full);
       }
-      if (ok && kr.nt == kr.n1) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->r_full, item & 1, w, kSiteRes));
+      // ------------------------------------------------------------ epilogue: the table's row, dQ rows
+      float res = 0.f;
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->r_full, item & 1, w, kSiteRes));
+      if (ok) {
         const float* s = sRes + (item & 1) * 256 + row;
         res = s[0] + s[128];
+        if (store && wg == 0) a.delta[tab] = nd - res;  // -(Delta' + r): both warpgroups have read it
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->ds_used, (n - 1) & 1, w, kSiteEpi));
       }
-      if (ok && store && wg == 0) a.delta[tab] = nd - res;  // -(Delta + r): both warpgroups have read it
-      // ------------------------------------------------------------ epilogue: dQ rows
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->dq_done[(n - 1) & 1], ((n - 1) >> 1) & 1, w, kSiteEpi));
       if (ok) {
         tc_fence_after();
         __nv_bfloat16* const dq0 = a.dq + (static_cast<size_t>(x.b) * g.S * g.Hq + x.h) * D;  // row 0 of the head
+        const float2 nr2 = make_float2(-res, -res), sc2 = make_float2(g.scale, g.scale);
 #pragma unroll 1
         for (int c0 = wg * (D / 2); c0 < (wg + 1) * (D / 2); c0 += 32) {
-          uint32_t o[32], pk[16];
-          tmem_ld32(trow + kColDQ + c0, o);
+          uint32_t o[32], p[32], pk[16];
+          tmem_ld32(trow + kColB + c0, o);
+          tmem_ld32(trow + C::kColA + c0, p);
           tmem_ld_wait();
           reg_fence32(o);
+          reg_fence32(p);
 #pragma unroll
-          for (int c = 0; c < 32; c += 2)
-            pk[c >> 1] = pack_bf16x2(__uint_as_float(o[c]) * g.scale, __uint_as_float(o[c + 1]) * g.scale);
+          for (int c = 0; c < 32; c += 2) {
+            const float2 y = fmul2(ffma2(make_float2(__uint_as_float(p[c]), __uint_as_float(p[c + 1])), nr2,
+                                         make_float2(__uint_as_float(o[c]), __uint_as_float(o[c + 1]))), sc2);
+            pk[c >> 1] = pack_bf16x2(y.x, y.y);
+          }
           store_rows32(dq0, static_cast<size_t>(g.Hq) * D, x.q0 + wq * 32, g.S, c0, pk);
         }
         ok = feed_take(bars->feed, item + 1, w, kSiteFeed, idx);
