@@ -469,8 +469,10 @@ int usp_window_attn_decode(const void* q, const void* k_cache, const void* v_cac
  *                (other strides, or one job's dst as another's src or dst, are
  *                refused; any other overlap is undefined).
  *   dtype        USP_BF16 or USP_F32 (arithmetic in fp32, rounded once)
- *   positions    DEVICE integers [n_axes][B][S], 32 or 64 bits (pos_bits); any sign
- *   inv_freq     HOST [R/2], radians per position step, finite
+ *   positions    DEVICE integers [n_axes][B][S], 32 or 64 bits (pos_bits); any sign.
+ *                The angle is off by less than |position| * 2^-64 turns beside the
+ *                rounding of the arithmetic (2^-24 turns at position 2^40)
+ *   inv_freq     HOST [R/2], radians per position step, finite, |inv_freq| <= 2^40
  *   axis         HOST [R/2], 0 .. n_axes-1
  *   paired       0: pairs (f, f + R/2); 1: pairs (2f, 2f + 1)
  * The layout does not matter: on rank-major or zigzag tensors, give the positions

@@ -471,8 +471,8 @@ def rope_axes(xs, positions, inv_freq, axis, paired: bool = False, inverse: bool
     """Rotary positions with several axes of the tensors xs (one or a sequence, [B, S, H_x, D], bf16 or
     fp32, any strides with the last dimension contiguous, e.g. q and k sliced from a fused projection),
     in one launch: pair f of every head row turns by positions[axis[f]] * inv_freq[f]. positions
-    [n_axes, B, S] int32 or int64 (CUDA); inv_freq [R/2] float64 and axis [R/2] int32 on the CPU (R <= D;
-    elements from R on are copied). paired: pairs (2f, 2f + 1) instead of (f, f + R/2). inverse: the
+    [n_axes, B, S] int32 or int64 (CUDA); inv_freq [R/2] float64, up to 2^40 radians per step, and axis
+    [R/2] int32 on the CPU (R <= D; elements from R on are copied). paired: pairs (2f, 2f + 1) instead of (f, f + R/2). inverse: the
     gradient's map. outs: where to write (may be xs: in place); else new contiguous tensors. Returns the
     list of outputs (one tensor for one tensor)."""
     single = isinstance(xs, torch.Tensor)

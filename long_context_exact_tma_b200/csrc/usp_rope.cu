@@ -7,9 +7,11 @@
 //
 // The angle of a far position needs more bits than fp32 has (at position 10^5 an
 // fp32 product is off by 4e-3 rad). Here it is counted in turns on 64 bits: the
-// host gives inv_freq / 2 pi as a 64-bit fraction of a turn, and the wrapping
-// 64-bit product with the position keeps the fraction of the turn exactly; its
-// upper 32 bits, as a signed number, are the angle within half a turn.
+// host gives inv_freq / 2 pi as a 64-bit fraction of a turn, off by less than one
+// count, and the wrapping 64-bit product with the position drops whole turns and
+// nothing else: the angle is off by less than |position| 2^-64 turns (2^-24 at
+// position 2^40). The product's upper 32 bits, as a signed number, are the angle
+// within half a turn.
 //
 // Bound by memory: each element is read and written once. A thread takes one
 // 16-byte chunk column (two in the halves form, of the copied rest too) of one token and walks some of its
@@ -232,8 +234,11 @@ cudaError_t launch(RopeArgs& a, long long tokens, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// inv_freq / 2 pi modulo 1 as a fraction of 2^64, to about 2^-64 of it (relative): the product
-// with 1 / 2 pi in two doubles, whole turns per position step dropped.
+// inv_freq / 2 pi modulo 1 as a fraction of 2^64, off by less than one count: the product with
+// 1 / 2 pi in two doubles, whole turns per position step dropped. That holds up to kMaxInvFreq: lo is the
+// part of a turn that the product's double leaves out, and from 2^43 on its own rounding shows in the
+// last count; past 2^52 it is more turns than the counts' 64 bits.
+constexpr double kMaxInvFreq = 1099511627776.0;  // 2^40
 unsigned long long turn_of(double inv_freq) {
   if (inv_freq < 0) return 0ull - turn_of(-inv_freq);
   constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;  // 1 / 2 pi and what its double leaves out
@@ -327,6 +332,8 @@ extern "C" int usp_rope_axes(const usp_rope_job* jobs, int n_jobs, int B, int S,
   a.axis_step = tokens;
   for (int f = 0; f < R / 2; ++f) {
     if (!isfinite(inv_freq[f])) return record_error(USP_ERR_INVALID_ARG, "inv_freq[%d] is not finite", f);
+    if (fabs(inv_freq[f]) > kMaxInvFreq)
+      return record_error(USP_ERR_UNSUPPORTED, "inv_freq[%d] = %g is past 2^40", f, inv_freq[f]);
     if (axis[f] < 0 || axis[f] >= n_axes) return record_error(USP_ERR_INVALID_ARG, "axis[%d] = %d is outside 0..%d", f, axis[f], n_axes - 1);
     a.turn[f] = turn_of(inv_freq[f]);
     a.axis[f] = static_cast<unsigned char>(axis[f]);
