@@ -401,8 +401,9 @@ def window_attn_fwd(q, k, v, window: int, sinks: int = 0, cu_seqlens=None, ws=No
         out = _like(out, "out", q, dev)
         lse = _lse_of(lse, q, geo[:3], dev)
         ws = _scratch(ws, B_.USP_WINDOW_FWD_WS, q, dev)
-        B_.call("usp_window_attn_fwd", q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), *geo,
-                None if cu_seqlens is None else cu_seqlens.data_ptr(), n_docs, ws.data_ptr(), ws.numel(), st)
+        B_.usp_window_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), *geo,
+                               None if cu_seqlens is None else cu_seqlens.data_ptr(), n_docs, ws.data_ptr(), ws.numel(),
+                               st)
         if check_status:
             check_workspace(ws, st)
     return out, lse
@@ -422,9 +423,10 @@ def window_attn_bwd(q, k, v, out, lse, dO, window: int, sinks: int = 0, cu_seqle
         dk = _like(dk, "dk", k, dev)
         dv = _like(dv, "dv", v, dev)
         ws = _scratch(ws, need, q, dev)
-        B_.call("usp_window_attn_bwd", q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                dO.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *geo,
-                None if cu_seqlens is None else cu_seqlens.data_ptr(), n_docs, ws.data_ptr(), ws.numel(), st)
+        B_.usp_window_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                               dO.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *geo,
+                               None if cu_seqlens is None else cu_seqlens.data_ptr(), n_docs, ws.data_ptr(), ws.numel(),
+                               st)
         if check_status:
             check_workspace(ws, st)
     return dq, dk, dv
@@ -461,9 +463,9 @@ def window_attn_decode(q, k_cache, v_cache, lens, window: int, sinks: int = 0, w
         lse = _lse_of(lse, q, (N, n, Hq), dev)
         # (the smallest size: the splits join in the launch itself and need none)
         ws = _scratch(ws, need, q, dev) if ws is not None or need > 256 else None
-        B_.call("usp_window_attn_decode", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), lens.data_ptr(),
-                out.data_ptr(), lse.data_ptr(), *geo, *ks[:3], *vs[:3], None if ws is None else ws.data_ptr(),
-                0 if ws is None else ws.numel(), st)
+        B_.usp_window_attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), lens.data_ptr(),
+                                  out.data_ptr(), lse.data_ptr(), *geo, ks[:3], vs[:3],
+                                  None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), st)
     return out, lse
 
 
@@ -525,8 +527,7 @@ def rope_axes(xs, positions, inv_freq, axis, paired: bool = False, inverse: bool
             if D > 1 and (sx[3] != 1 or sy[3] != 1):
                 raise ValueError("the last dimension must be contiguous")
             ys.append(y)
-            jobs.append(B_.ROPE_JOB.pack(x.data_ptr(), y.data_ptr(), H, *sx[:3], *sy[:3]))
-        B_.call("usp_rope_axes", b"".join(jobs), n, B, S, D, 2 * n_freq, dt, positions.data_ptr(),
-                64 if pos_type is torch.int64 else 32, pos_shape[0], inv_freq.data_ptr(), axis.data_ptr(),
-                1 if paired else 0, 1 if inverse else 0, st)
+            jobs.append((x.data_ptr(), y.data_ptr(), H, sx[:3], sy[:3]))
+        B_.usp_rope_axes(jobs, B, S, D, 2 * n_freq, dt, positions.data_ptr(), 64 if pos_type is torch.int64 else 32,
+                         pos_shape[0], inv_freq.data_ptr(), axis.data_ptr(), 1 if paired else 0, 1 if inverse else 0, st)
     return ys[0] if single else ys

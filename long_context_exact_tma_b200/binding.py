@@ -67,7 +67,8 @@ class RopeJob(ctypes.Structure):
                 ("d_b", ctypes.c_longlong), ("d_t", ctypes.c_longlong), ("d_h", ctypes.c_longlong)]
 
 
-ROPE_JOB = struct.Struct("@PPi6q")  # the same, as bytes
+# the same, packed: filling a ctypes structure would take longer than the launch itself
+ROPE_JOB = struct.Struct("@" + "".join(t._type_ for _, t in RopeJob._fields_))
 
 
 class PermuteJob(ctypes.Structure):
@@ -180,14 +181,6 @@ def _check(rc: int) -> int:
     if rc != USP_OK:
         raise UspError(rc, lib().usp_last_error().decode())
     return rc
-
-
-def call(name: str, *args) -> None:
-    """The C call of that name with addresses and numbers as they are (for callers that have them at
-    hand: on a call of a few microseconds the functions below cost one more); raises on a bad status."""
-    rc = getattr(_lib or lib(), name)(*args)
-    if rc != USP_OK:
-        _check(rc)
 
 
 def usp_version() -> int:
@@ -317,18 +310,19 @@ def usp_window_workspace_size(B, S, Hq, Hkv, D, window, sinks, n_docs, bwd) -> i
     return int(lib().usp_window_workspace_size(B, S, Hq, Hkv, D, window, sinks, n_docs, int(bwd)))
 
 
+# The calls of a few microseconds: pointers as addresses (None: null), and the raw stream, since what it
+# takes to get these from tensors in between shows in such a call.
 def usp_window_attn_fwd(q, k, v, out, lse, B, S, Hq, Hkv, D, window, sinks, cu_seqlens, n_docs, workspace, ws_bytes,
-                        stream=None, check=True):
-    rc = lib().usp_window_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, S, Hq, Hkv, D, window, sinks,
-                                   _ptr(cu_seqlens), n_docs, _ptr(workspace), ws_bytes, _stream(stream))
+                        stream, check=True):
+    rc = (_lib or lib()).usp_window_attn_fwd(q, k, v, out, lse, B, S, Hq, Hkv, D, window, sinks, cu_seqlens, n_docs,
+                                             workspace, ws_bytes, stream)
     return _check(rc) if check else rc
 
 
 def usp_window_attn_bwd(q, k, v, out, lse, dO, dQ, dK, dV, B, S, Hq, Hkv, D, window, sinks, cu_seqlens, n_docs,
-                        workspace, ws_bytes, stream=None, check=True):
-    rc = lib().usp_window_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dO), _ptr(dQ), _ptr(dK),
-                                   _ptr(dV), B, S, Hq, Hkv, D, window, sinks, _ptr(cu_seqlens), n_docs,
-                                   _ptr(workspace), ws_bytes, _stream(stream))
+                        workspace, ws_bytes, stream, check=True):
+    rc = (_lib or lib()).usp_window_attn_bwd(q, k, v, out, lse, dO, dQ, dK, dV, B, S, Hq, Hkv, D, window, sinks,
+                                             cu_seqlens, n_docs, workspace, ws_bytes, stream)
     return _check(rc) if check else rc
 
 
@@ -337,22 +331,20 @@ def usp_window_decode_workspace_size(N, n, cap, Hq, Hkv, D, window, sinks) -> in
 
 
 def usp_window_attn_decode(q, k_cache, v_cache, lens, out, lse, N, n, cap, Hq, Hkv, D, window, sinks, k_strides,
-                           v_strides, workspace, ws_bytes, stream=None, check=True):
+                           v_strides, workspace, ws_bytes, stream, check=True):
     """k_strides, v_strides: (sequence, token, head) strides of the caches in elements."""
-    rc = lib().usp_window_attn_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(lens), _ptr(out), _ptr(lse), N, n,
-                                      cap, Hq, Hkv, D, window, sinks, *k_strides, *v_strides, _ptr(workspace),
-                                      ws_bytes, _stream(stream))
+    rc = (_lib or lib()).usp_window_attn_decode(q, k_cache, v_cache, lens, out, lse, N, n, cap, Hq, Hkv, D, window,
+                                                sinks, *k_strides, *v_strides, workspace, ws_bytes, stream)
     return _check(rc) if check else rc
 
 
-def usp_rope_axes(jobs, B, S, D, R, dtype, positions, pos_bits, n_axes, inv_freq, axis, paired, inverse, stream=None,
+def usp_rope_axes(jobs, B, S, D, R, dtype, positions, pos_bits, n_axes, inv_freq, axis, paired, inverse, stream,
                   check=True):
     """jobs: sequence of (src, dst, H, (s_b, s_t, s_h), (d_b, d_t, d_h)); inv_freq (float64) and axis (int32) in
     host memory: CPU tensors or addresses."""
-    # (packed by hand: ctypes structures would take longer to fill than the launch itself)
-    arr = b"".join([ROPE_JOB.pack(_ptr(src) or 0, _ptr(dst) or 0, H, *ss, *ds) for src, dst, H, ss, ds in jobs])
-    rc = lib().usp_rope_axes(arr, len(jobs), B, S, D, R, dtype, _ptr(positions), pos_bits, n_axes, _ptr(inv_freq),
-                             _ptr(axis), int(paired), int(inverse), _stream(stream))
+    arr = b"".join([ROPE_JOB.pack(src or 0, dst or 0, H, *ss, *ds) for src, dst, H, ss, ds in jobs])
+    rc = (_lib or lib()).usp_rope_axes(arr, len(jobs), B, S, D, R, dtype, positions, pos_bits, n_axes, _ptr(inv_freq),
+                                       _ptr(axis), paired, inverse, stream)
     return _check(rc) if check else rc
 
 
