@@ -273,7 +273,6 @@ cudaError_t launch_d(const WinLaunch& L, cudaStream_t stream) {
   a.delta = L.delta;
   a.Lp = L.Lp;
   a.part = L.far_part;
-  const long long heads = static_cast<long long>(L.g.Hkv) * L.g.B;
   a.chunk = L.far_chunk;
   a.n_chunks = (L.g.n_tiles + a.chunk - 1) / a.chunk;
   const long long n_far = static_cast<long long>(L.g.Hkv) * L.g.B * a.n_chunks;
