@@ -147,8 +147,8 @@ __device__ __forceinline__ void store_rows32(__nv_bfloat16* base, size_t row_ste
 
 // ---------------------------------------------------------------- work items
 // Hands a persistent CTA its work items: the first is its block number, each next one
-// the grid's counter says when the CTA is ready for it (items differ: documents, rows
-// walked twice, short walks at the start of a sequence). One warp asks ahead; the
+// the grid's counter says when the CTA is ready for it (items differ: documents,
+// short walks at the start of a sequence). One warp asks ahead; the
 // others take the number from a slot.
 struct ItemFeed {
   uint64_t full[2], empty[2];

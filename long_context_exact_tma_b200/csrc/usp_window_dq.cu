@@ -25,9 +25,11 @@
 // dP are issued behind this one's last products, and its first A and B wait for P and
 // dS, written by the warps that read this item's A and B before them.
 //
-// Bound at D=128 by the chain S -> P -> A -> S of the one S buffer, beside four products that take
-// 1.1 us. Backward of 32768 tokens, 16/4 heads, W=2048, 4 sinks: 1916 us against 1769 with the three
-// products; W=8, where every row had walked its keys twice: 107 against 136.
+// Bound by the compute warps' two phases, one behind the other, and four products that
+// take 1.1 us of the 1.8 us per key tile (tensor pipe 60 % active), and by about 3.5 us per
+// item. B=1 S=32768 H=16/4 D=128 W=2048, 4 sinks: 930 us, 861 TFLOP/s of 6 D flops per visible
+// pair (8 D with A); with the three products 761. Backward of 8192 tokens, W=8, where every row
+// had walked its keys twice for the residue: 107 us against 136.
 #include <math.h>
 
 #include "usp_ptx.cuh"
