@@ -15,8 +15,8 @@
 //   dQ_i / scale = sum_j dS'_ij k_j - r_i sum_j P_ij k_j = B_i - r_i A_i.
 // A is a fourth product beside the three, for every row: without it dQ is off by
 // r_i A_i, which stands beside a dQ that cancels alike wherever a row's keys or
-// values have much in common (one key with most of the weight, a common part,
-// repeated tokens; 10 to 50 times the rounding of dS in such rows), not only where a
+// values have much in common (one key with most of the weight, a common part, or
+// repeated tokens: 4 to 49 times the bound of the roundings in such rows), not only where a
 // row has few keys. r and A are good to 2^-8, so what is left of r is as small beside
 // it as a rounding. Delta_i goes back to the table, for the key-major kernels that run after.
 //
